@@ -386,6 +386,68 @@ DSA_API dsa_status_t dsa_masked_mha_fwd(const void* q, const void* k, const void
 /* Device workspace bytes for dsa_masked_mha_fwd (0 for invalid sizes). */
 DSA_API size_t dsa_masked_mha_workspace_size(int64_t total_q, int max_len_k);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Serving from a paged latent cache.  The pages describe the latent cache
+ * ("DeepSeek-V3.2" atlas entry, "Inference efficiency": MLA keeps one latent
+ * per token, shared by all query heads) and leave its layout open; these calls
+ * take the layout serving engines keep it in:
+ *
+ *  kv_cache (device) bf16 pool of n_pages pages of page_size rows of 576;
+ *           page i starts page_stride elements after page i - 1 (page_stride
+ *           >= page_size * 576, a multiple of 8; larger when a page holds
+ *           several layers).  page_size is a multiple of 16.
+ *  block_table (device) int32, max_pages entries in row b at block_table +
+ *           b * block_table_ld: entry j names the pool page that holds entries
+ *           [j * page_size, (j+1) * page_size) of sequence b.  Only the pages a
+ *           sequence's length reaches are read.  Sequences may share pages.
+ *  seq_lens (device) int32 [B]: entries cached per sequence, the newest token's
+ *           own among them; 0 is allowed.  Rows of a page behind the length
+ *           are never used, whatever they hold.
+ *  max_len_k bounds the lengths (at most 2^24).
+ *
+ * A length outside [0, min(max_len_k, max_pages * page_size)] is cut to that
+ * range, and a page id outside the pool reads as rows of zeros; both set
+ * DSA_ERR_BOUNDS in the device error word.
+ *
+ * window, sinks: with window = 0 the newest token (position len - 1) sees the
+ * whole sequence; with window > 0 it sees its last `window` entries, itself
+ * included, and the first `sinks` entries of the sequence.
+ * ---------------------------------------------------------------------------
+ *
+ * Attention of one new token per sequence, MQA mode of MLA:
+ *
+ *   out[b, h, :] = sum_s softmax_s(sm_scale * q[b,h,:] . x[s]) * x[s, 0:d_v]
+ *   lse[b, h]    = log sum_s exp(sm_scale * q[b,h,:] . x[s])
+ *
+ * over the entries s it sees (x[s] the cached latent).  A sequence of length 0
+ * gets out = 0 and lse = -inf.
+ *
+ *  q        (device) bf16 [B, H, 576]
+ *  out      (device) bf16 [B, H, 512]
+ *  lse      (device, nullable) f32 [B, H] (natural log)
+ *  workspace (device) dsa_paged_mla_decode_workspace_size bytes, 16-byte
+ *           aligned; what it holds before a call does not matter.  Calls that
+ *           may overlap on the GPU need one each.
+ *  Supported: d_qk = 576, d_v = 512, H in {16, 32} or a multiple of 64 up to
+ *  256.
+ *  Arithmetic: bf16 tensor-core products, fp32 accumulation and softmax (the
+ *  weights are rounded to bf16 for the product with the values).  The result
+ *  does not depend on timing: a sequence split over the GPU is joined in a
+ *  fixed order.
+ */
+DSA_API dsa_status_t dsa_paged_mla_decode(const void* q, const void* kv_cache, int64_t n_pages,
+                                          int page_size, int64_t page_stride,
+                                          const int32_t* block_table, int64_t block_table_ld,
+                                          int max_pages, const int32_t* seq_lens, int B, int max_len_k, int H,
+                                          int d_qk, int d_v, int window, int sinks,
+                                          float sm_scale, void* out, float* lse, void* workspace,
+                                          size_t workspace_bytes, void* stream);
+
+/* Device workspace bytes for dsa_paged_mla_decode: the parts of sequences that
+ * are split over the GPU.  Returns 0 for invalid sizes. */
+DSA_API size_t dsa_paged_mla_decode_workspace_size(int B, int H, int max_len_k);
+
 /* Bytes of workspace dsa_forward needs: an f32 score matrix [total_q,
  * round_up(max_len_k, 4)] plus an int32 index matrix [total_q, k], each
  * 256-byte aligned.  Returns 0 for invalid sizes. */

@@ -18,7 +18,8 @@ __all__ = [
     "dsa_forward_host", "dsa_forward_host_workspace_size", "dsa_indexer_kl",
     "dsa_indexer_kl_workspace_size", "dsa_masked_mha_fwd", "dsa_masked_mha_workspace_size",
     "dsa_debug_fault_injection", "dsa_indexer_backward", "dsa_forward_fused",
-    "dsa_forward_fused_workspace_size", "EXPORTED",
+    "dsa_forward_fused_workspace_size", "dsa_paged_mla_decode",
+    "dsa_paged_mla_decode_workspace_size", "EXPORTED",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -32,7 +33,8 @@ EXPORTED = (
     "dsa_forward_noalloc", "dsa_forward_host", "dsa_forward_host_workspace_size",
     "dsa_indexer_kl", "dsa_indexer_kl_workspace_size", "dsa_masked_mha_fwd",
     "dsa_masked_mha_workspace_size", "dsa_debug_fault_injection", "dsa_indexer_backward",
-    "dsa_forward_fused", "dsa_forward_fused_workspace_size",
+    "dsa_forward_fused", "dsa_forward_fused_workspace_size", "dsa_paged_mla_decode",
+    "dsa_paged_mla_decode_workspace_size",
 )
 
 STATUS = {
@@ -98,6 +100,11 @@ def load():
     lib.dsa_indexer_backward.argtypes = [P, P, P, P, P, P, I64, P, P, I, I, I, I64, I64, I, I, P,
                                          P, P, P]
     lib.dsa_indexer_backward.restype = I
+    lib.dsa_paged_mla_decode.argtypes = [P, P, I64, I, I64, P, I64, I, P, I, I, I, I, I, I, I, F,
+                                         P, P, P, ctypes.c_size_t, P]
+    lib.dsa_paged_mla_decode.restype = I
+    lib.dsa_paged_mla_decode_workspace_size.argtypes = [I, I, I]
+    lib.dsa_paged_mla_decode_workspace_size.restype = ctypes.c_size_t
     lib.dsa_debug_fault_injection.argtypes = [ctypes.c_uint64, I]
     lib.dsa_debug_fault_injection.restype = None
     lib.dsa_version.argtypes = []
@@ -440,6 +447,91 @@ def dsa_masked_mha_fwd(q, k, v, idx, cu_seqlens_q, cu_seqlens_k, B, max_len_q, m
                                    int(topk), float(sm_scale), _ptr(out), _ptr(lse),
                                    _ptr(workspace), int(workspace.numel()), _stream(stream))
     _check(rc, "dsa_masked_mha_fwd")
+
+
+def _stream_on(stream, device):
+    """The torch stream a call runs on: the given one (a torch stream or a raw
+    handle), or the device's current stream."""
+    import torch
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if hasattr(stream, "cuda_stream"):
+        return stream
+    return torch.cuda.ExternalStream(int(stream), device=device)
+
+
+def _paged(kv_cache, block_table, seq_lens, **others):
+    """Checks the tensors of a call over a paged cache against each other and
+    returns the cache's arguments in the C ABI's order."""
+    import torch
+    if kv_cache.dim() != 3 or kv_cache.shape[2] != 576:
+        raise ValueError("kv_cache must be [n_pages, page_size, 576]")
+    if kv_cache.dtype != torch.bfloat16 or not kv_cache.is_cuda:
+        raise ValueError("kv_cache must be a CUDA torch.bfloat16 tensor")
+    if kv_cache.stride(2) != 1 or (kv_cache.shape[1] > 1 and kv_cache.stride(1) != 576):
+        raise ValueError("kv_cache rows must be contiguous within a page")
+    if kv_cache.shape[0] > 1 and kv_cache.stride(0) < 0:
+        raise ValueError("kv_cache pages must be in memory order")
+    _need(seq_lens, torch.int32, "seq_lens", 1)
+    B = seq_lens.shape[0]
+    tables = {"block_table": block_table}
+    tables.update((k, v) for k, v in others.items() if k.endswith("block_table"))
+    for name, t in tables.items():
+        if t.dim() != 2 or t.dtype != torch.int32 or not t.is_cuda or t.shape[0] != B:
+            raise ValueError(f"{name} must be a CUDA torch.int32 tensor [B, pages]")
+        if t.shape[1] > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name} rows must be contiguous")
+    for name, t in {"block_table": block_table, "seq_lens": seq_lens, **others}.items():
+        if t is not None and t.device != kv_cache.device:
+            raise ValueError(f"{name} must be on kv_cache's device, {kv_cache.device}")
+    n_pages, page = kv_cache.shape[:2]
+    stride = kv_cache.stride(0) if n_pages > 1 else page * 576
+    return (_ptr(kv_cache), int(n_pages), int(page), int(stride), _ptr(block_table),
+            _table_ld(block_table), int(block_table.shape[1]), _ptr(seq_lens), int(B))
+
+
+def _table_ld(t):
+    return int(t.stride(0)) if t.shape[0] > 1 else int(t.shape[1])
+
+
+def _shape(t, shape, name):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def dsa_paged_mla_decode_workspace_size(B, H, max_len_k) -> int:
+    return int(load().dsa_paged_mla_decode_workspace_size(int(B), int(H), int(max_len_k)))
+
+
+def dsa_paged_mla_decode(q, kv_cache, block_table, seq_lens, max_len_k, sm_scale, out, lse=None,
+                         window=0, sinks=0, workspace=None, stream=None):
+    """Attention of one new token per sequence, q [B, H, 576], over a paged
+    latent cache (see include/dsa.h): kv_cache [n_pages, page_size, 576] (pages
+    may be strided), block_table [B, pages], seq_lens [B].  Writes out
+    [B, H, 512] (bf16) and lse [B, H] (fp32, optional).  window > 0 limits a
+    token to its last `window` entries and the first `sinks`.  `workspace`
+    (uint8 CUDA tensor) is allocated here, on the call's stream, when not
+    given."""
+    import torch
+    _need(q, torch.bfloat16, "q", 3)
+    _need(out, torch.bfloat16, "out", 3)
+    _need(lse, torch.float32, "lse", 2)
+    _need(workspace, torch.uint8, "workspace")
+    cache = _paged(kv_cache, block_table, seq_lens, q=q, out=out, lse=lse, workspace=workspace)
+    B, H, d_qk = q.shape
+    _shape(q, (seq_lens.shape[0], H, d_qk), "q")
+    _shape(out, (B, H, out.shape[2]), "out")
+    _shape(lse, (B, H), "lse")
+    st = _stream_on(stream, q.device)
+    with torch.cuda.device(q.device), torch.cuda.stream(st):
+        if workspace is None:
+            nbytes = dsa_paged_mla_decode_workspace_size(B, H, max_len_k)
+            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+        rc = load().dsa_paged_mla_decode(
+            _ptr(q), *cache, int(max_len_k), int(H), int(d_qk), int(out.shape[2]), int(window),
+            int(sinks), float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace),
+            int(workspace.numel()), ctypes.c_void_p(st.cuda_stream))
+    _check(rc, "dsa_paged_mla_decode")
 
 
 def dsa_get_device_error(stream=None) -> int:

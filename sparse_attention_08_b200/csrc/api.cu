@@ -104,6 +104,21 @@ dsa_status_t encode_3d_bf16(CUtensorMap* m, const void* base, uint64_t d0, uint6
   return r == CUDA_SUCCESS ? DSA_OK : DSA_ERR_CUDA;
 }
 
+// The pool of pages as a 3D tensor [n_pages, page, 576] of bf16 (pages
+// page_stride elements apart), box 64 x box_rows x 1, 128-byte swizzle.
+dsa_status_t encode_pool(CUtensorMap* m, const void* base, int64_t n_pages, int page,
+                         int64_t page_stride, int box_rows) {
+  const cuuint64_t dims[3] = {576, static_cast<cuuint64_t>(page), static_cast<cuuint64_t>(n_pages)};
+  const cuuint64_t strides[2] = {576 * 2, static_cast<cuuint64_t>(page_stride) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? DSA_OK : DSA_ERR_CUDA;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 dsa_status_t check_varlen(const int32_t* cu_q, const int32_t* cu_k, int B, int max_len_q,
@@ -665,6 +680,92 @@ dsa_status_t dsa_forward_fused(const void* q_fp8, const float* q_scale, const fl
   if ((st = from_cuda(dsa::launch_topk(tka, next_err(dev), s))) != DSA_OK) return st;
   return dsa_sparse_mla_fwd(q, kv, idx, cu_seqlens_q, cu_seqlens_k, B, max_len_q, max_len_k,
                             total_q, total_k, H, d_qk, d_v, k, sm_scale, out, lse, stream);
+}
+
+namespace {
+
+// The arguments that every call over a paged cache takes.
+dsa_status_t check_cache(const void* kv_cache, int64_t n_pages, int page_size,
+                         int64_t page_stride, const int32_t* block_table, int64_t block_table_ld,
+                         int max_pages, const int32_t* seq_lens, int B, int max_len_k) {
+  if (!kv_cache || !block_table || !seq_lens || B < 0 || max_len_k < 0 || n_pages < 1 ||
+      page_size < 1 || max_pages < 1 || block_table_ld < max_pages)
+    return DSA_ERR_INVALID_ARG;
+  if (page_size % 16 != 0 || page_size > (1 << 20) || n_pages >= (int64_t(1) << 31) ||
+      max_len_k > (1 << 24))
+    return DSA_ERR_UNSUPPORTED;
+  if (page_stride < static_cast<int64_t>(page_size) * 576) return DSA_ERR_INVALID_ARG;
+  if (page_stride >= (int64_t(1) << 38)) return DSA_ERR_UNSUPPORTED;
+  if (!aligned16(kv_cache) || page_stride % 8 != 0) return DSA_ERR_ALIGNMENT;
+  if (static_cast<int64_t>(B) * (max_len_k / 128 + 1) >= (int64_t(1) << 31))
+    return DSA_ERR_UNSUPPORTED;
+  return DSA_OK;
+}
+
+dsa::paged::Cache cache_of(int64_t n_pages, int page_size, const int32_t* block_table,
+                           int64_t block_table_ld, int max_pages, const int32_t* seq_lens, int B,
+                           int max_len_k, int window, int sinks) {
+  dsa::paged::Cache c;
+  c.table = block_table;
+  c.lens = seq_lens;
+  c.table_ld = block_table_ld;
+  c.B = B;
+  c.page = page_size;
+  const int low = page_size & -page_size;
+  c.box = low < 128 ? low : 128;
+  c.n_pages = static_cast<int>(n_pages);
+  const int64_t held = static_cast<int64_t>(max_pages) * page_size;
+  c.cap = held < max_len_k ? static_cast<int>(held) : max_len_k;
+  c.window = window;
+  c.sinks = sinks;
+  return c;
+}
+
+}  // namespace
+
+size_t dsa_paged_mla_decode_workspace_size(int B, int H, int max_len_k) {
+  if (B < 0 || !mla_heads_ok(H) || max_len_k < 0 || max_len_k > (1 << 24)) return 0;
+  return dsa::paged_decode_workspace_bytes(B, H, max_len_k);
+}
+
+dsa_status_t dsa_paged_mla_decode(const void* q, const void* kv_cache, int64_t n_pages,
+                                  int page_size, int64_t page_stride, const int32_t* block_table,
+                                  int64_t block_table_ld, int max_pages,
+                                  const int32_t* seq_lens, int B, int max_len_k, int H, int d_qk, int d_v, int window, int sinks,
+                                  float sm_scale, void* out, float* lse, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  if (!q || !out || window < 0 || sinks < 0) return DSA_ERR_INVALID_ARG;
+  if (d_qk != 576 || d_v != 512 || !mla_heads_ok(H)) return DSA_ERR_UNSUPPORTED;
+  dsa_status_t st = check_cache(kv_cache, n_pages, page_size, page_stride, block_table,
+                                block_table_ld, max_pages, seq_lens, B, max_len_k);
+  if (st != DSA_OK) return st;
+  if (!(sm_scale > 0.f) || sm_scale != sm_scale) return DSA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out) || (workspace && !aligned16(workspace)))
+    return DSA_ERR_ALIGNMENT;
+  if (static_cast<int64_t>(B) * H >= (int64_t(1) << 31)) return DSA_ERR_UNSUPPORTED;
+  if (B == 0) return DSA_OK;
+  if (!workspace || workspace_bytes < dsa::paged_decode_workspace_bytes(B, H, max_len_k))
+    return DSA_ERR_WORKSPACE;
+  DeviceInfo* dev = nullptr;
+  if ((st = device_info(&dev)) != DSA_OK) return st;
+  dsa::PagedDecodeArgs a;
+  a.cache = cache_of(n_pages, page_size, block_table, block_table_ld, max_pages, seq_lens, B,
+                     max_len_k, window, sinks);
+  a.H = H;
+  a.max_len_k = max_len_k;
+  a.sm_scale = sm_scale;
+  a.out = out;
+  a.lse = lse;
+  a.workspace = workspace;
+  CUtensorMap tq, tx;
+  if ((st = encode_2d(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q, static_cast<uint64_t>(B) * H, 576,
+                      2, H < 64 ? static_cast<uint32_t>(H) : 64u, 64,
+                      CU_TENSOR_MAP_SWIZZLE_128B)) != DSA_OK)
+    return st;
+  if ((st = encode_pool(&tx, kv_cache, n_pages, page_size, page_stride, a.cache.box)) != DSA_OK)
+    return st;
+  return from_cuda(
+      dsa::launch_paged_decode(tq, tx, a, next_err(dev), static_cast<cudaStream_t>(stream)));
 }
 
 void dsa_debug_fault_injection(uint64_t wait_limit_ns, int drop_first_key_load) {

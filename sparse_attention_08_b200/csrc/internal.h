@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "paged.cuh"
 #include "ptx.cuh"
 
 namespace dsa {
@@ -180,5 +181,18 @@ cudaError_t launch_masked_mha(const CUtensorMap& tq, const CUtensorMap& tk, cons
                               const MaskedMhaArgs& a, DevErr err, cudaStream_t s);
 size_t masked_mha_workspace_bytes(int64_t total_q, int max_len_k);
 size_t indexer_kl_workspace_bytes(int64_t total_q, int H, int k);
+
+// ---- operators over a paged latent cache
+struct PagedDecodeArgs {
+  paged::Cache cache;
+  int H, max_len_k;
+  float sm_scale;
+  void* out;
+  float* lse;        // nullable
+  void* workspace;   // paged_decode_workspace_bytes
+};
+cudaError_t launch_paged_decode(const CUtensorMap& tq, const CUtensorMap& tx,
+                                const PagedDecodeArgs& a, DevErr err, cudaStream_t s);
+size_t paged_decode_workspace_bytes(int B, int H, int max_len_k);
 
 }  // namespace dsa

@@ -1,0 +1,211 @@
+// paged.cuh -- what the kernels over a paged latent cache share: which keys a
+// sequence's newest token sees, how those tiles are dealt out to the CTAs, and
+// the loads of one tile through the block table.
+//
+// A cache is a pool of pages of `page` latent rows; row s of sequence b is row
+// s % page of pool page table[b, s / page].  The newest token of a sequence of
+// n entries sees all of them, or (window > 0) the entries s >= n - window and
+// s < sinks.  Keys are worked on in tiles of 128 positions; the tiles that
+// hold a seen key are numbered 0 .. n_tiles-1 within the sequence.
+#pragma once
+
+#include "ptx.cuh"
+
+namespace dsa {
+namespace paged {
+
+constexpr int kTile = 128;                      // keys per tile
+constexpr int kChunks = 9;                      // 64-column chunks of a 576-d row
+constexpr uint32_t kChunkBytes = kTile * 128;   // one chunk of a tile: 16 KB
+
+struct Cache {
+  const int32_t* table;    // [B, table_ld]
+  const int32_t* lens;     // [B]
+  int64_t table_ld;
+  int B;
+  int page;                // rows per page, a multiple of 16
+  int box;                 // rows per TMA box: the largest power of two <= 128 that divides page
+  int n_pages;             // pages in the pool
+  int cap;                 // longest sequence the call allows
+  int window, sinks;
+};
+
+// The length of sequence b, kept inside [0, cap].
+__device__ __forceinline__ int seq_len(const Cache& c, int b) {
+  return min(max(__ldg(c.lens + b), 0), c.cap);
+}
+
+// The tiles of a sequence that hold a seen key: the first `a` tiles (the
+// first tokens), then tiles from `w0` on (the window).
+struct Seen {
+  int len, lo, ns;   // seen: s < ns or lo <= s < len
+  int a, w0, n;
+  __device__ __forceinline__ int tile(int i) const { return i < a ? i : w0 + (i - a); }
+  __device__ __forceinline__ bool key(int s) const { return s < ns || (s >= lo && s < len); }
+  // any seen key in [s, s + rows)?
+  __device__ __forceinline__ bool any(int s, int rows) const {
+    return s < ns || (s < len && s + rows > lo);
+  }
+};
+
+__device__ __forceinline__ Seen seen_of(const Cache& c, int len) {
+  Seen k;
+  k.len = len;
+  k.lo = c.window > 0 ? max(0, len - c.window) : 0;
+  k.ns = min(c.sinks, k.lo);
+  k.a = (k.ns + kTile - 1) / kTile;
+  k.w0 = max(k.lo / kTile, k.a);
+  k.n = k.a + (len + kTile - 1) / kTile - k.w0;
+  return k;
+}
+
+// Sum over the warp, the same in every lane.
+__device__ __forceinline__ int warp_sum(int v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+
+// The tiles of all sequences in one line, cut into `ranges` pieces of `per`
+// tiles (the last ones shorter or empty).  min_tiles = 1 gives a sequence
+// without a seen key one (empty) tile, so that somebody writes its output.
+struct Start {
+  int b;         // sequence of the piece's first tile (B: the piece is empty)
+  int skip;      // its tiles that belong to earlier pieces
+  int per;       // tiles per piece
+};
+
+// Called by every thread of the CTA (nwarps whole warps); scratch: nwarps + 3 ints.
+// Warp w adds up sequences [w, w+1) * B / nwarps; the warp whose stretch holds
+// the piece's first tile then finds its sequence with a scan.
+__device__ __forceinline__ Start find_start(const Cache& c, int range, int ranges, int min_tiles,
+                                            int nwarps, int* scratch, const DevErr& err) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int each = ((c.B + nwarps - 1) / nwarps + 31) / 32 * 32;
+  const int b0 = min(c.B, warp * each), b1 = min(c.B, b0 + each);
+  int sum = 0;
+  bool bad = false;
+  for (int b = b0 + lane; b < b1; b += 32) {
+    const int raw = __ldg(c.lens + b);
+    bad |= raw < 0 || raw > c.cap;
+    sum += max(seen_of(c, seq_len(c, b)).n, min_tiles);
+  }
+  if (bad && range == 0) raise_error(err, kErrBounds);
+  sum = warp_sum(sum);
+  if (lane == 0) scratch[warp] = sum;
+  if (threadIdx.x == 0) scratch[nwarps] = c.B;
+  __syncthreads();
+  int total = 0, before = 0;
+  for (int w = 0; w < nwarps; ++w) {
+    if (w < warp) before += scratch[w];
+    total += scratch[w];
+  }
+  const int per = max(1, (total + ranges - 1) / ranges);
+  const int first = min(static_cast<int64_t>(range) * per, static_cast<int64_t>(total));
+  if (first < total && first >= before && first < before + sum) {
+    for (int b = b0; b < b1; b += 32) {
+      const int n = b + lane < b1 ? max(seen_of(c, seq_len(c, b + lane)).n, min_tiles) : 0;
+      int inc = n;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += v;
+      }
+      const int end = before + inc;
+      if (first >= end - n && first < end) {
+        scratch[nwarps] = b + lane;
+        scratch[nwarps + 1] = first - (end - n);
+      }
+      before += __shfl_sync(0xffffffffu, inc, 31);
+      if (before > first) break;
+    }
+  }
+  __syncthreads();
+  Start s;
+  s.b = scratch[nwarps];
+  s.skip = scratch[nwarps + 1];
+  s.per = per;
+  return s;
+}
+
+// Walks the tiles of one piece, segment by segment (a segment: the piece's
+// share of one sequence).  Every role of a CTA walks the same way.
+struct Walk {
+  const Cache& c;
+  int b, i0, i1, left, min_tiles;
+  Seen k;
+  __device__ __forceinline__ Walk(const Cache& cache, const Start& s, int min_t)
+      : c(cache), b(s.b), i0(s.skip), i1(0), left(s.per), min_tiles(min_t) {}
+  // Moves to the next segment: sequence b, its tiles [i0, i1).
+  __device__ __forceinline__ bool next(bool first) {
+    if (!first) {
+      ++b;
+      i0 = 0;
+    }
+    for (; left > 0 && b < c.B; ++b) {
+      k = seen_of(c, seq_len(c, b));
+      const int n = max(k.n, min_tiles);
+      if (n > i0) {
+        i1 = min(n, i0 + left);
+        left -= i1 - i0;
+        return true;
+      }
+      i0 = 0;
+    }
+    return false;
+  }
+};
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, int32_t x, int32_t y,
+                                            int32_t z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// What a lane of the loading warp brings in of one tile: box `lane` of the
+// tile's 128 / box boxes, if it holds a seen key.
+struct Box {
+  bool on;
+  int32_t page, row;
+};
+
+__device__ __forceinline__ Box box_of(const Cache& c, const Seen& k, int b, int tile, int lane,
+                                      const DevErr& err) {
+  Box x;
+  const int s = tile * kTile + lane * c.box;
+  x.on = lane * c.box < kTile && k.any(s, c.box);
+  x.page = 0;
+  x.row = 0;
+  if (x.on) {
+    x.page = __ldg(c.table + static_cast<int64_t>(b) * c.table_ld + s / c.page);
+    x.row = s % c.page;
+    // an id outside the pool reads zeros (the copy's own bounds check)
+    if (x.page < 0 || x.page >= c.n_pages) raise_error(err, kErrBounds);
+  }
+  return x;
+}
+
+// Sums (or maxima) of 32 columns over the lanes of a warp: lane i ends with
+// column i's, in 31 shuffles.
+template <bool kMax>
+__device__ __forceinline__ float column_reduce(float (&v)[32]) {
+  const int lane = threadIdx.x % 32;
+#pragma unroll
+  for (int half = 16; half > 0; half >>= 1) {
+    const bool up = (lane & half) != 0;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float send = up ? v[i] : v[i + half];
+      const float keep = up ? v[i + half] : v[i];
+      const float got = __shfl_xor_sync(0xffffffffu, send, half);
+      v[i] = kMax ? fmaxf(keep, got) : keep + got;
+    }
+  }
+  return v[0];
+}
+
+}  // namespace paged
+}  // namespace dsa

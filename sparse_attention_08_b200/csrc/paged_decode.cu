@@ -1,0 +1,568 @@
+// paged_decode.cu -- attention of one new token per sequence over a paged
+// latent cache, in the MQA mode of MLA, on sm_100a.
+//
+// What it computes (b a sequence, h a head, x[s] the 576-d latent of entry s,
+// its first 512 dims the value, V_b the entries the newest token sees):
+//
+//   out[b,h,:] = sum_{s in V_b} softmax_s(scale q[b,h,:] . x[s]) x[s, 0:512]
+//   lse[b,h]   = log sum_{s in V_b} exp(scale q[b,h,:] . x[s])
+//
+// One CTA works on up to 64 heads and a run of 128-key tiles.  The products
+// are formed with the KEYS (and then the value dims) as the MMA's 128 rows and
+// the heads as its columns:
+//
+//   S^T [128 keys x 64 heads]     = X [128 x 576] Q^T       36 MMAs, M128 N64 K16
+//   O^T [4 x 128 dims x 64 heads] += X[:, 0:512]^T P^T       32 MMAs, M128 N64 K16
+//
+// With the heads as rows a 64-head CTA could only issue M = 64 MMAs, which take
+// as long as M = 128 ones, and twice the time of these.  The latents are read
+// from shared memory as they lie: rows of 64-column chunks are K-major for
+// S^T and, transposed, MN-major for O^T.  A thread then holds one key and the
+// heads' scores side by side, so P^T (a key's 64 heads in 128 bytes) is written
+// as whole 16-byte pieces of an MN-major operand, without a transpose.
+//
+// The softmax needs no maximum over the lanes on the common path: any
+// reference m[h] within 2^16 of the row's maximum serves (P is bf16 and O fp32,
+// both with an 8-bit exponent), so a tile only votes whether a score exceeds
+// its reference by more; then the columns' maxima are reduced over the lanes
+// and O^T and the sums are rescaled.
+//
+// Shared memory: the heads' queries (72 KB) and one tile (nine 16 KB chunks,
+// each with its own full and empty barrier).  P^T overwrites the RoPE chunk,
+// which the values do not need.  A chunk is reloaded as soon as its product is
+// done, so the next tile streams in behind O^T's products; 148 CTAs at
+// different points of that cycle keep the memory busy.
+//
+// The sequences' tiles stand in one line that is cut into equal pieces, one
+// per CTA (times the head groups, which read the same keys at the same time, so
+// the second finds them in L2).  A sequence inside one piece is finished there; the
+// parts of a split one go to the workspace and combine_kernel joins them in
+// the order of the pieces, so the result does not depend on timing.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "internal.h"
+#include "paged.cuh"
+#include "ptx.cuh"
+
+namespace dsa {
+namespace {
+
+using namespace paged;
+
+constexpr int kHeads = 64;                            // heads per CTA (MMA N)
+constexpr int kDv = 512;
+constexpr uint32_t kQChunk = kHeads * 128;            // 8 KB
+constexpr uint32_t kOffX = 0;                         // the tile
+constexpr uint32_t kOffP = kOffX + 8 * kChunkBytes;   // P^T over the RoPE chunk
+constexpr uint32_t kOffQ = kOffX + kChunks * kChunkBytes;
+constexpr uint32_t kOffBar = kOffQ + kChunks * kQChunk;
+// barriers: full[9], empty[9], q_full, q_empty, s_full, p_full, o_full, o_empty, drain
+constexpr uint32_t kNumBars = 2 * kChunks + 7;
+constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;         // TMEM slot, plan scratch
+constexpr uint32_t kOffRef = (kOffMisc + 80 + 127) / 128 * 128;   // m[64], alpha[64]
+constexpr uint32_t kOffRed = kOffRef + 2 * kHeads * 4;        // [2][4][64]
+constexpr uint32_t kSmem = kOffRed + 8 * kHeads * 4 + 1024;
+constexpr int kWarps = 10;
+constexpr int kThreads = 32 * kWarps;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 0;                         // + 64 * (dims / 128)
+constexpr uint32_t kColS = 256;
+constexpr uint32_t kIdescS = instr_desc(kFmtBF16, kFmtBF16, 0, 0, 128, kHeads);
+constexpr uint32_t kIdescO = instr_desc(kFmtBF16, kFmtBF16, 1, 1, 128, kHeads);
+constexpr float kSlack = 16.0f;                       // log2 units above the reference
+constexpr float kNoRef = -1e30f;                      // no score yet: any finite one is above
+constexpr float kLn2 = 0.69314718055994531f;
+
+static_assert(kSmem <= 232448, "shared memory budget");
+
+struct Params {
+  Cache c;
+  int H, groups, pieces;
+  float scale_log2;
+  __nv_bfloat16* out;   // [B, H, 512]
+  float* lse;           // [B, H], nullable
+  int32_t* plan;        // workspace: [B] first tile of each sequence, [B] tiles per piece
+  float4* ml;           // workspace: [2 * pieces * groups][64] reference, sums
+  float* part;          // workspace: [2 * pieces * groups][64][512] unnormalised O
+  DevErr err;
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_decode_kernel(const __grid_constant__ CUtensorMap tq,
+                        const __grid_constant__ CUtensorMap tx, const Params P) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + kOffBar;
+  auto full = [&](int i) { return bar0 + 8u * i; };
+  auto empty = [&](int i) { return bar0 + 8u * (kChunks + i); };
+  const uint32_t q_full = bar0 + 8u * (2 * kChunks);
+  const uint32_t q_empty = q_full + 8, s_full = q_full + 16, p_full = q_full + 24;
+  const uint32_t o_full = q_full + 32, o_empty = q_full + 40, drain = q_full + 48;
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + kOffMisc);
+  int* scratch = reinterpret_cast<int*>(smem + kOffMisc + 16);
+  float* ref = reinterpret_cast<float*>(smem + kOffRef);
+  float* alpha = ref + kHeads;
+  float* red = reinterpret_cast<float*>(smem + kOffRed);
+
+  const int warp = threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  const int g = blockIdx.x % P.groups;
+  const int piece = blockIdx.x / P.groups;
+  const int heads = min(kHeads, P.H - g * kHeads);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kChunks; ++i) {
+      mbar_init(full(i), 1);
+      mbar_init(empty(i), 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    mbar_init(s_full, 1);
+    mbar_init(p_full, 8);
+    mbar_init(o_full, 1);
+    mbar_init(o_empty, 8);
+    mbar_init(drain, 1);
+    fence_barrier_init();
+    tma_prefetch_desc(&tq);
+    tma_prefetch_desc(&tx);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), kTmemCols);
+    tmem_relinquish();
+  }
+  // query rows past the last head stay zero (their columns are never stored)
+  if (heads < kHeads)
+    for (uint32_t i = threadIdx.x; i < kChunks * kQChunk / 16; i += kThreads)
+      reinterpret_cast<uint4*>(smem + kOffQ)[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  tc_fence_before();
+  const Start start = find_start(P.c, piece, P.pieces, 1, kWarps, scratch, P.err);
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (blockIdx.x == 0 && threadIdx.x == 0) P.plan[P.c.B] = start.per;
+  Walk w(P.c, start, 1);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ loads
+    // Lane i brings in box i of a tile, chunk by chunk; lane 0 waits for the
+    // chunk to be free and announces the bytes.
+    uint32_t n = 0;               // tiles so far
+    bool ok = true;
+    int seg = 0, stop = 0;        // segments whose queries, chunks of tile n that were asked for
+    for (; ok && w.next(seg == 0); ++seg) {
+      if (seg > 0) ok = warp_wait(q_empty, (seg - 1) & 1, P.err);
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(q_full, kChunks * static_cast<uint32_t>(heads) * 128);
+        for (int c = 0; c < kChunks; ++c)
+          tma_load_2d(sbase + kOffQ + c * kQChunk, &tq, 64 * c, w.b * P.H + g * kHeads, q_full);
+      }
+      Box x = box_of(P.c, w.k, w.b, w.k.tile(w.i0), lane, P.err);
+      for (int i = w.i0; i < w.i1; ++i, ++n) {
+        Box nx;                   // the next tile's page ids, fetched a tile ahead
+        nx.on = false;
+        if (i + 1 < w.i1) nx = box_of(P.c, w.k, w.b, w.k.tile(i + 1), lane, P.err);
+        const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, x.on));
+        const uint32_t dst = sbase + kOffX + static_cast<uint32_t>(lane * P.c.box) * 128;
+        for (int c = 0; c < kChunks; ++c) {
+          ok = warp_wait(empty(c), (n & 1) ^ 1, P.err);
+          if (!ok) {
+            stop = c;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(full(c), boxes * static_cast<uint32_t>(P.c.box) * 128);
+          __syncwarp();
+          if (x.on) tma_load_3d(dst + c * kChunkBytes, &tx, 64 * c, x.row, x.page, full(c));
+        }
+        if (!ok) break;
+        x = nx;
+      }
+      if (!ok) {
+        ++seg;
+        break;
+      }
+    }
+    // after a failure, let the copies in flight land before the memory goes
+    if (!ok && lane == 0) {
+      if (seg > 0) mbar_wait_drain(q_full, (seg - 1) & 1, P.err);
+      for (int c = 0; c < kChunks; ++c) {
+        const uint32_t asked = n + (c < stop ? 1 : 0);
+        if (asked > 0) mbar_wait_drain(full(c), (asked - 1) & 1, P.err);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA
+    if (lane == 0) {
+      const uint64_t dXk = smem_desc(sbase + kOffX, 16, 1024, kSwizzle128B);
+      const uint64_t dQ = smem_desc(sbase + kOffQ, 16, 1024, kSwizzle128B);
+      const uint64_t dXv = smem_desc(sbase + kOffX, kChunkBytes, 1024, kSwizzle128B);
+      const uint64_t dP = smem_desc(sbase + kOffP, kChunkBytes, 1024, kSwizzle128B);
+      uint32_t n = 0;
+      bool ok = true;
+      for (int seg = 0; ok && w.next(seg == 0); ++seg) {
+        ok = mbar_wait(q_full, seg & 1, P.err);
+        for (int i = w.i0; ok && i < w.i1; ++i, ++n) {
+#pragma unroll 1
+          for (int c = 0; ok && c < kChunks; ++c) {
+            ok = mbar_wait(full(c), n & 1, P.err);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_f16(tmem + kColS, dXk + ((c * kChunkBytes + kk * 32) >> 4),
+                      dQ + ((c * kQChunk + kk * 32) >> 4), kIdescS, (c | kk) != 0 ? 1u : 0u);
+          }
+          if (!ok) break;
+          mma_commit(s_full);
+          if (i + 1 == w.i1) mma_commit(q_empty);
+          // the last segment's O^T must have been read out
+          if (i == w.i0 && seg > 0) ok = mbar_wait(o_empty, (seg - 1) & 1, P.err);
+          ok = ok && mbar_wait(p_full, n & 1, P.err);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int mt = 0; mt < 4; ++mt) {
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              mma_f16(tmem + kColO + 64u * mt, dXv + ((mt * 2 * kChunkBytes + kk * 2048) >> 4),
+                      dP + ((kk * 2048) >> 4), kIdescO, (i > w.i0 || kk > 0) ? 1u : 0u);
+            mma_commit(empty(2 * mt));
+            mma_commit(empty(2 * mt + 1));
+          }
+          mma_commit(empty(8));
+          if (i + 1 == w.i1) mma_commit(o_full);
+        }
+      }
+      mma_commit(drain);
+      mbar_wait_drain(drain, 0, P.err);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax
+    // Two warpgroups; a thread owns one key of the tile (TMEM lane) and 32 of
+    // the heads.
+    const int wg = (warp - 2) >> 2;
+    const int sp = warp & 3;                          // TMEM sub-partition
+    const int r = sp * 32 + lane;                     // key in the tile
+    const int tid = threadIdx.x - 64;                 // 0..255
+    const uint32_t lane_base = static_cast<uint32_t>(sp * 32) << 16;
+    const int h0 = 32 * wg;
+    uint8_t* prow = smem + kOffP + r * 128;
+    uint32_t n = 0;
+    bool ok = true;
+    for (int seg = 0; ok && w.next(seg == 0); ++seg) {
+      float2 l[16], lr[16];       // sums of P and of P as rounded to bf16
+#pragma unroll
+      for (int e = 0; e < 16; ++e) l[e] = lr[e] = make_float2(0.f, 0.f);
+      for (int i = w.i0; i < w.i1; ++i, ++n) {
+        const int tile = w.k.tile(i);
+        const bool seen = w.k.key(tile * kTile + r);
+        const bool bad = !warp_wait(s_full, n & 1, P.err);
+        uint32_t v[32];
+        bool over = false;
+        if (!bad) {
+          tc_fence_after();
+          tmem_ld_32x32b_x32(tmem + lane_base + kColS + h0, v);
+          tmem_wait_ld();
+          tc_fence_before();
+        }
+        if (!seen)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = 0xff800000u;
+        const float2 sc = make_float2(P.scale_log2, P.scale_log2);
+        if (i > w.i0) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 m = *reinterpret_cast<const float4*>(ref + h0 + e);
+            top = fmaxf(top, __uint_as_float(v[e]) * P.scale_log2 - m.x);
+            top = fmaxf(top, __uint_as_float(v[e + 1]) * P.scale_log2 - m.y);
+            top = fmaxf(top, __uint_as_float(v[e + 2]) * P.scale_log2 - m.z);
+            top = fmaxf(top, __uint_as_float(v[e + 3]) * P.scale_log2 - m.w);
+          }
+          over = top > kSlack;
+        }
+        // one vote for all eight warps; it also takes them out together when
+        // a wait of one of them gave up
+        if (named_bar_or(1, 256, bad || over) || i == w.i0) {
+          if (named_bar_or(1, 256, bad)) {
+            ok = false;
+            break;
+          }
+          // new references: the columns' maxima over the tile
+          float m[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) m[e] = __uint_as_float(v[e]) * P.scale_log2;
+          red[sp * kHeads + h0 + lane] = column_reduce<true>(m);
+          named_bar_sync(1, 256);
+          if (tid < kHeads) {
+            const float old = i > w.i0 ? ref[tid] : kNoRef;
+            const float top = fmaxf(fmaxf(red[tid], red[kHeads + tid]),
+                                    fmaxf(red[2 * kHeads + tid], red[3 * kHeads + tid]));
+            const float now = fmaxf(old, top);
+            alpha[tid] = fast_exp2(old - now);
+            ref[tid] = now;
+          }
+          named_bar_sync(1, 256);
+          if (i > w.i0) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float2 al = *reinterpret_cast<const float2*>(alpha + h0 + 2 * e);
+              l[e] = __fmul2_rn(l[e], al);
+              lr[e] = __fmul2_rn(lr[e], al);
+            }
+            // every earlier product is complete: this tile's last chunk could
+            // only be loaded after it
+#pragma unroll 1
+            for (int mt = 0; mt < 4; ++mt) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(tmem + lane_base + kColO + 64u * mt + h0, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha[h0 + e]);
+              tmem_st_32x32b_x32(tmem + lane_base + kColO + 64u * mt + h0, o);
+            }
+            tmem_wait_st();
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
+          uint32_t pk[4];
+#pragma unroll
+          for (int u = 0; u < 8; u += 2) {
+            const float2 m = *reinterpret_cast<const float2*>(ref + h0 + e + u);
+            const float2 y = __ffma2_rn(make_float2(__uint_as_float(v[e + u]),
+                                                    __uint_as_float(v[e + u + 1])),
+                                        sc, make_float2(-m.x, -m.y));
+            const float2 p = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+            const int a = (e + u) / 2;
+            l[a] = __fadd2_rn(l[a], p);
+            const uint32_t b = pack_bf16x2(p.x, p.y);
+            pk[u / 2] = b;
+            lr[a] = __fadd2_rn(lr[a], make_float2(__uint_as_float(b << 16),
+                                                  __uint_as_float(b & 0xFFFF0000u)));
+          }
+          *reinterpret_cast<uint4*>(prow + (((h0 + e) / 8) ^ (r & 7)) * 16) =
+              make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        }
+        // an unseen row of the tile holds whatever its memory held: its
+        // weight is 0, and so must its value be (0 * NaN is not)
+        if (!seen) {
+#pragma unroll 1
+          for (int c = 4 * wg; c < 4 * wg + 4; ++c)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<uint4*>(smem + kOffX + c * kChunkBytes + r * 128 + (j ^ (r & 7)) * 16) =
+                  make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full);
+      }
+      if (!ok) break;
+      // ---------------------------------------------------------- read-out
+      float ls[32], ls2[32];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        ls[2 * e] = l[e].x;
+        ls[2 * e + 1] = l[e].y;
+        ls2[2 * e] = lr[e].x;
+        ls2[2 * e + 1] = lr[e].y;
+      }
+      red[sp * kHeads + h0 + lane] = column_reduce<false>(ls);
+      red[4 * kHeads + sp * kHeads + h0 + lane] = column_reduce<false>(ls2);
+      const bool bad = !warp_wait(o_full, seg & 1, P.err);
+      if (named_bar_or(1, 256, bad)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const int tiles = max(w.k.n, 1);
+      const bool whole = w.i0 == 0 && w.i1 == tiles;
+      const int64_t slot = (static_cast<int64_t>(piece) * 2 + (seg == 0 ? 0 : 1)) * P.groups + g;
+      if (tid < heads) {
+        float sum = 0.f, sumr = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sum += red[e * kHeads + tid];
+          sumr += red[(4 + e) * kHeads + tid];
+        }
+        const int64_t at = static_cast<int64_t>(w.b) * P.H + g * kHeads + tid;
+        if (whole) {
+          if (P.lse) P.lse[at] = sum == 0.f ? -INFINITY : (ref[tid] + log2f(sum)) * kLn2;
+        } else {
+          P.ml[slot * kHeads + tid] = make_float4(ref[tid], sum, sumr, 0.f);
+        }
+        alpha[tid] = sumr == 0.f ? 0.f : 1.f / sumr;
+      }
+      if (w.i0 == 0 && g == 0 && tid == 0)
+        P.plan[w.b] = piece * start.per + start.per - w.left - (w.i1 - w.i0);
+      named_bar_sync(1, 256);
+#pragma unroll 1
+      for (int mt = 0; mt < 4; ++mt) {
+        uint32_t o[32];
+        tmem_ld_32x32b_x32(tmem + lane_base + kColO + 64u * mt + h0, o);
+        tmem_wait_ld();
+        if (whole) {
+          // lanes hold neighbouring dims: pairs of lanes swap so that each
+          // stores two dims of one head
+          const int d = mt * 128 + sp * 32 + (lane & ~1);
+          __nv_bfloat16* dst = P.out + (static_cast<int64_t>(w.b) * P.H + g * kHeads + h0) * kDv + d;
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 iv = *reinterpret_cast<const float2*>(alpha + h0 + e);
+            const float a = __uint_as_float(o[e]) * iv.x, b = __uint_as_float(o[e + 1]) * iv.y;
+            const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? a : b, 1);
+            const int h = e + (lane & 1);
+            if (h0 + h < heads)
+              *reinterpret_cast<uint32_t*>(dst + static_cast<int64_t>(h) * kDv) =
+                  (lane & 1) ? pack_bf16x2(got, b) : pack_bf16x2(a, got);
+          }
+        } else {
+          float* dst = P.part + (slot * kHeads + h0) * kDv + mt * 128 + r;
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (h0 + e < heads) dst[e * kDv] = __uint_as_float(o[e]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_empty);
+      // the references and sums are read above; the next segment rewrites them
+      named_bar_sync(1, 256);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Joins the parts of the sequences that were split: with the parts'
+// references m_i and M their maximum, out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
+// One CTA per (head, sequence), a thread four value dims.
+constexpr int kMaxParts = 160;
+__global__ void __launch_bounds__(128) combine_kernel(const Params P) {
+  __shared__ float wt[kMaxParts];
+  __shared__ float tot[3];
+  const int h = blockIdx.x;
+  const int b = blockIdx.y + gridDim.y * blockIdx.z;
+  if (b >= P.c.B) return;
+  const int per = P.plan[P.c.B];
+  const int t0 = P.plan[b];
+  const int n = max(seen_of(P.c, seq_len(P.c, b)).n, 1);
+  const int r0 = t0 / per, r1 = (t0 + n - 1) / per;
+  if (r0 == r1) return;
+  const int parts = r1 - r0 + 1;
+  const int g = h / kHeads, hh = h % kHeads;
+  auto slot = [&](int i) {
+    return (static_cast<int64_t>(r0 + i) * 2 + (i == 0 && t0 > r0 * per ? 1 : 0)) * P.groups + g;
+  };
+  if (threadIdx.x < 32) {
+    float top = -INFINITY;
+    for (int i = threadIdx.x; i < parts; i += 32) {
+      const float4 x = P.ml[slot(i) * kHeads + hh];
+      if (x.y != 0.f) top = fmaxf(top, x.x);          // a part without a weight has no reference
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    float l = 0.f, lr = 0.f;
+    for (int i = threadIdx.x; i < parts; i += 32) {
+      const float4 x = P.ml[slot(i) * kHeads + hh];
+      const float f = x.y != 0.f ? exp2f(x.x - top) : 0.f;
+      wt[i] = f;
+      l += f * x.y;
+      lr += f * x.z;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      l += __shfl_xor_sync(0xffffffffu, l, d);
+      lr += __shfl_xor_sync(0xffffffffu, lr, d);
+    }
+    if (threadIdx.x == 0) {
+      tot[0] = l;
+      tot[1] = lr == 0.f ? 0.f : 1.f / lr;
+      tot[2] = top;
+    }
+  }
+  __syncthreads();
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = 0; i < parts; ++i) {
+    const float4 x = *reinterpret_cast<const float4*>(P.part + (slot(i) * kHeads + hh) * kDv + 4 * threadIdx.x);
+    const float f = wt[i];
+    o.x += f * x.x;
+    o.y += f * x.y;
+    o.z += f * x.z;
+    o.w += f * x.w;
+  }
+  const float inv = tot[1];
+  const int64_t row = static_cast<int64_t>(b) * P.H + h;
+  *reinterpret_cast<uint2*>(P.out + row * kDv + 4 * threadIdx.x) =
+      make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  if (threadIdx.x == 0 && P.lse)
+    P.lse[row] = tot[0] == 0.f ? -INFINITY : (tot[2] + log2f(tot[0])) * kLn2;
+}
+
+constexpr int kMaxCtas = 148;
+
+int groups_of(int H) { return (H + kHeads - 1) / kHeads; }
+
+// Pieces the tile line is cut into: one CTA per SM over all head groups, and
+// no more than there can be tiles.
+int pieces_of(int B, int H, int max_len_k) {
+  const int64_t each = (max_len_k + kTile - 1) / kTile;
+  const int64_t tiles = static_cast<int64_t>(B) * (each > 0 ? each : 1);
+  const int64_t most = kMaxCtas / groups_of(H);
+  return static_cast<int>(tiles < most ? tiles : most);
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+
+size_t paged_decode_workspace_bytes(int B, int H, int max_len_k) {
+  const size_t slots = static_cast<size_t>(2) * pieces_of(B, H, max_len_k) * groups_of(H);
+  return up256((static_cast<size_t>(B) + 1) * 4) + slots * kHeads * (16 + kDv * 4);
+}
+
+cudaError_t launch_paged_decode(const CUtensorMap& tq, const CUtensorMap& tx,
+                                const PagedDecodeArgs& a, DevErr err, cudaStream_t s) {
+  Params P;
+  P.c = a.cache;
+  P.H = a.H;
+  P.groups = groups_of(a.H);
+  P.pieces = pieces_of(a.cache.B, a.H, a.max_len_k);
+  P.scale_log2 = a.sm_scale * 1.4426950408889634f;
+  P.out = static_cast<__nv_bfloat16*>(a.out);
+  P.lse = a.lse;
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  P.plan = reinterpret_cast<int32_t*>(ws);
+  ws += up256((static_cast<size_t>(a.cache.B) + 1) * 4);
+  P.ml = reinterpret_cast<float4*>(ws);
+  ws += static_cast<size_t>(2) * P.pieces * P.groups * kHeads * 16;
+  P.part = reinterpret_cast<float*>(ws);
+  P.err = err;
+  cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(kSmem));
+  if (e != cudaSuccess) return e;
+  paged_decode_kernel<<<static_cast<unsigned>(P.pieces * P.groups), kThreads, kSmem, s>>>(tq, tx, P);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (a.max_len_k <= kTile) return cudaSuccess;     // one tile per sequence: nothing is split
+  const unsigned y = a.cache.B < 65535 ? static_cast<unsigned>(a.cache.B) : 65535u;
+  const unsigned z = (static_cast<unsigned>(a.cache.B) + y - 1) / y;
+  combine_kernel<<<dim3(static_cast<unsigned>(a.H), y, z), 128, 0, s>>>(P);
+  return cudaGetLastError();
+}
+
+}  // namespace dsa

@@ -1,0 +1,71 @@
+"""What the calls over a paged cache refuse, on the host, before any launch."""
+import ctypes
+
+import pytest
+import torch
+
+import sparse_attention_08_b200 as dsa
+
+OK, INVALID, UNSUPPORTED, ALIGN, WORKSPACE, CUDA = 0, 1, 2, 3, 4, 5
+P = ctypes.c_void_p(0x10000)
+
+
+def off(n):
+    return ctypes.c_void_p(0x10000 + n)
+
+
+CACHE = dict(kv=P, n_pages=100, page=64, stride=64 * 576, table=P, ld=10, pages=10, lens=P, B=4,
+             max_len=640)
+
+
+def cache_args(a):
+    return [a[k] for k in ("kv", "n_pages", "page", "stride", "table", "ld", "pages", "lens", "B",
+                           "max_len")]
+
+
+BAD_CACHE = [
+    (dict(kv=None), INVALID), (dict(table=None), INVALID), (dict(lens=None), INVALID),
+    (dict(B=-1), INVALID), (dict(max_len=-1), INVALID), (dict(n_pages=0), INVALID),
+    (dict(page=0), INVALID), (dict(pages=0), INVALID), (dict(ld=9), INVALID),
+    (dict(stride=64 * 576 - 8), INVALID),
+    (dict(page=8), UNSUPPORTED), (dict(page=63), UNSUPPORTED), (dict(page=1), UNSUPPORTED),
+    (dict(max_len=(1 << 24) + 1), UNSUPPORTED), (dict(n_pages=1 << 31), UNSUPPORTED),
+    (dict(kv=off(8)), ALIGN), (dict(stride=64 * 576 + 4), ALIGN),
+]
+
+
+def decode(**kw):
+    a = dict(CACHE, q=P, H=128, d_qk=576, d_v=512, window=0, sinks=0, scale=0.04, out=P, lse=P,
+             ws=P, nbytes=1 << 40)
+    a.update(kw)
+    return dsa.load().dsa_paged_mla_decode(a["q"], *cache_args(a), a["H"], a["d_qk"], a["d_v"],
+                                           a["window"], a["sinks"], a["scale"], a["out"], a["lse"],
+                                           a["ws"], a["nbytes"], None)
+
+
+@pytest.mark.parametrize("kw,status", BAD_CACHE + [
+    (dict(q=None), INVALID), (dict(out=None), INVALID), (dict(window=-1), INVALID),
+    (dict(sinks=-1), INVALID), (dict(scale=0.0), INVALID), (dict(scale=float("nan")), INVALID),
+    (dict(H=8), UNSUPPORTED), (dict(H=320), UNSUPPORTED), (dict(d_qk=512), UNSUPPORTED),
+    (dict(d_v=576), UNSUPPORTED), (dict(q=off(2)), ALIGN), (dict(out=off(8)), ALIGN),
+    (dict(ws=None), WORKSPACE), (dict(nbytes=100), WORKSPACE), (dict(ws=off(4)), ALIGN),
+    (dict(B=0), OK),
+])
+def test_decode_refuses(kw, status):
+    assert decode(**kw) == status
+
+
+def test_decode_workspace_size():
+    size = dsa.dsa_paged_mla_decode_workspace_size
+    assert size(1, 128, 131072) >= 2 * 148 * 64 * (512 * 4 + 16)
+    assert size(1, 128, 100) < size(1, 128, 131072)
+    assert size(-1, 128, 100) == 0 and size(1, 100, 100) == 0 and size(1, 128, -1) == 0
+
+
+def test_wrappers_check_tensors():
+    t = torch.zeros
+    with pytest.raises(ValueError):         # CPU tensors
+        dsa.dsa_paged_mla_decode(t((1, 16, 576), dtype=torch.bfloat16),
+                                 t((2, 16, 576), dtype=torch.bfloat16),
+                                 t((1, 2), dtype=torch.int32), t(1, dtype=torch.int32), 32, 0.04,
+                                 t((1, 16, 512), dtype=torch.bfloat16))
