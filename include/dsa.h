@@ -396,7 +396,8 @@ DSA_API size_t dsa_masked_mha_workspace_size(int64_t total_q, int max_len_k);
  *  kv_cache (device) bf16 pool of n_pages pages of page_size rows of 576;
  *           page i starts page_stride elements after page i - 1 (page_stride
  *           >= page_size * 576, a multiple of 8; larger when a page holds
- *           several layers).  page_size is a multiple of 16.
+ *           several layers).  page_size is a multiple of 16, at
+ *           most 65536.
  *  block_table (device) int32, max_pages entries in row b at block_table +
  *           b * block_table_ld: entry j names the pool page that holds entries
  *           [j * page_size, (j+1) * page_size) of sequence b.  Only the pages a

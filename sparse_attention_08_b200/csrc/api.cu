@@ -691,7 +691,7 @@ dsa_status_t check_cache(const void* kv_cache, int64_t n_pages, int page_size,
   if (!kv_cache || !block_table || !seq_lens || B < 0 || max_len_k < 0 || n_pages < 1 ||
       page_size < 1 || max_pages < 1 || block_table_ld < max_pages)
     return DSA_ERR_INVALID_ARG;
-  if (page_size % 16 != 0 || page_size > (1 << 20) || n_pages >= (int64_t(1) << 31) ||
+  if (page_size % 16 != 0 || page_size > 65536 || n_pages >= (int64_t(1) << 31) ||
       max_len_k > (1 << 24))
     return DSA_ERR_UNSUPPORTED;
   if (page_stride < static_cast<int64_t>(page_size) * 576) return DSA_ERR_INVALID_ARG;
@@ -702,15 +702,19 @@ dsa_status_t check_cache(const void* kv_cache, int64_t n_pages, int page_size,
   return DSA_OK;
 }
 
-dsa::paged::Cache cache_of(int64_t n_pages, int page_size, const int32_t* block_table,
-                           int64_t block_table_ld, int max_pages, const int32_t* seq_lens, int B,
+dsa::paged::Cache cache_of(const void* kv_cache, int64_t n_pages, int page_size,
+                           int64_t page_stride, const int32_t* block_table, int64_t block_table_ld,
+                           int max_pages, const int32_t* seq_lens, int B,
                            int max_len_k, int window, int sinks) {
   dsa::paged::Cache c;
+  c.pool = static_cast<const uint8_t*>(kv_cache);
+  c.page_stride = page_stride;
   c.table = block_table;
   c.lens = seq_lens;
   c.table_ld = block_table_ld;
   c.B = B;
   c.page = page_size;
+  c.page_inv = ((uint64_t(1) << 43) + page_size - 1) / page_size;
   const int low = page_size & -page_size;
   c.box = low < 128 ? low : 128;
   c.n_pages = static_cast<int>(n_pages);
@@ -749,8 +753,8 @@ dsa_status_t dsa_paged_mla_decode(const void* q, const void* kv_cache, int64_t n
   DeviceInfo* dev = nullptr;
   if ((st = device_info(&dev)) != DSA_OK) return st;
   dsa::PagedDecodeArgs a;
-  a.cache = cache_of(n_pages, page_size, block_table, block_table_ld, max_pages, seq_lens, B,
-                     max_len_k, window, sinks);
+  a.cache = cache_of(kv_cache, n_pages, page_size, page_stride, block_table, block_table_ld,
+                     max_pages, seq_lens, B, max_len_k, window, sinks);
   a.H = H;
   a.max_len_k = max_len_k;
   a.sm_scale = sm_scale;

@@ -27,9 +27,9 @@
 // its reference by more; then the columns' maxima are reduced over the lanes
 // and O^T and the sums are rescaled.
 //
-// Shared memory: the heads' queries (72 KB) and one tile (nine 16 KB chunks,
-// each with its own full and empty barrier).  P^T overwrites the RoPE chunk,
-// which the values do not need.  A chunk is reloaded as soon as its product is
+// Shared memory: the heads' queries (72 KB) and one tile (nine 16 KB chunks
+// in five parts with their own full and empty barriers).  P^T overwrites the
+// RoPE chunk, which the values do not need.  A part is reloaded as soon as its product is
 // done, so the next tile streams in behind O^T's products; 148 CTAs at
 // different points of that cycle keep the memory busy.
 //
@@ -58,13 +58,18 @@ constexpr uint32_t kOffX = 0;                         // the tile
 constexpr uint32_t kOffP = kOffX + 8 * kChunkBytes;   // P^T over the RoPE chunk
 constexpr uint32_t kOffQ = kOffX + kChunks * kChunkBytes;
 constexpr uint32_t kOffBar = kOffQ + kChunks * kQChunk;
-// barriers: full[9], empty[9], q_full, q_empty, s_full, p_full, o_full, o_empty, drain
-constexpr uint32_t kNumBars = 2 * kChunks + 7;
+constexpr int kParts = 5;                             // chunk pairs 0..3, the RoPE chunk
+// barriers: full[3] (parts 0 and 1, parts 2 and 3, part 4), empty[5], q_full, q_empty, s_full, p_full, o_full, o_empty, drain
+constexpr uint32_t kNumBars = 3 + kParts + 7;
 constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;         // TMEM slot, plan scratch
-constexpr uint32_t kOffRef = (kOffMisc + 80 + 127) / 128 * 128;   // m[64], alpha[64]
-constexpr uint32_t kOffRed = kOffRef + 2 * kHeads * 4;        // [2][4][64]
-constexpr uint32_t kSmem = kOffRed + 8 * kHeads * 4 + 1024;
-constexpr int kWarps = 10;
+constexpr uint32_t kOffRef = (kOffMisc + 128 + 127) / 128 * 128;   // -m[64], alpha[64]
+constexpr uint32_t kOffRed = kOffRef + 2 * kHeads * 4;        // [4][64]
+constexpr uint32_t kSmem = kOffRed + 4 * kHeads * 4 + 1024;
+constexpr int kLoaders = 3;                           // loading warps: warp i brings in parts i, i + 3
+constexpr int kSoft = 16;                             // softmax warps: four warpgroups
+constexpr int kWide = kHeads * 4 / kSoft;             // heads per softmax thread
+constexpr int kSoftThreads = 32 * kSoft;
+constexpr int kWarps = kLoaders + 1 + kSoft;
 constexpr int kThreads = 32 * kWarps;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0;                         // + 64 * (dims / 128)
@@ -84,7 +89,7 @@ struct Params {
   __nv_bfloat16* out;   // [B, H, 512]
   float* lse;           // [B, H], nullable
   int32_t* plan;        // workspace: [B] first tile of each sequence, [B] tiles per piece
-  float4* ml;           // workspace: [2 * pieces * groups][64] reference, sums
+  float2* ml;           // workspace: [2 * pieces * groups][64] reference, sum
   float* part;          // workspace: [2 * pieces * groups][64][512] unnormalised O
   DevErr err;
 };
@@ -97,9 +102,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bar0 = sbase + kOffBar;
-  auto full = [&](int i) { return bar0 + 8u * i; };
-  auto empty = [&](int i) { return bar0 + 8u * (kChunks + i); };
-  const uint32_t q_full = bar0 + 8u * (2 * kChunks);
+  auto full = [&](int part) { return bar0 + 8u * (part / 2); };
+  auto empty = [&](int i) { return bar0 + 8u * (3 + i); };
+  const uint32_t q_full = bar0 + 8u * (3 + kParts);
   const uint32_t q_empty = q_full + 8, s_full = q_full + 16, p_full = q_full + 24;
   const uint32_t o_full = q_full + 32, o_empty = q_full + 40, drain = q_full + 48;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + kOffMisc);
@@ -115,27 +120,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int heads = min(kHeads, P.H - g * kHeads);
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kChunks; ++i) {
-      mbar_init(full(i), 1);
-      mbar_init(empty(i), 1);
-    }
+    mbar_init(full(0), 2);
+    mbar_init(full(2), 2);
+    mbar_init(full(4), 1);
+    for (int i = 0; i < kParts; ++i) mbar_init(empty(i), 1);
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     mbar_init(s_full, 1);
-    mbar_init(p_full, 8);
+    mbar_init(p_full, kSoft);
     mbar_init(o_full, 1);
-    mbar_init(o_empty, 8);
+    mbar_init(o_empty, kSoft);
     mbar_init(drain, 1);
     fence_barrier_init();
     tma_prefetch_desc(&tq);
     tma_prefetch_desc(&tx);
   }
-  if (warp == 1) {
+  if (warp == kLoaders) {
     tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), kTmemCols);
     tmem_relinquish();
   }
   // query rows past the last head stay zero (their columns are never stored)
   if (heads < kHeads)
+#pragma unroll 1
     for (uint32_t i = threadIdx.x; i < kChunks * kQChunk / 16; i += kThreads)
       reinterpret_cast<uint4*>(smem + kOffQ)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
@@ -146,37 +152,51 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (blockIdx.x == 0 && threadIdx.x == 0) P.plan[P.c.B] = start.per;
   Walk w(P.c, start, 1);
 
-  if (warp == 0) {
+  if (warp < kLoaders) {
     // ------------------------------------------------------------ loads
-    // Lane i brings in box i of a tile, chunk by chunk; lane 0 waits for the
-    // chunk to be free and announces the bytes.
+    // Lane i brings in box i of each of the warp's parts of a tile.  One warp
+    // alone would take longer over a tile's waits and copies (about 300
+    // cycles a part) than the tile's products leave between their parts.
     uint32_t n = 0;               // tiles so far
     bool ok = true;
-    int seg = 0, stop = 0;        // segments whose queries, chunks of tile n that were asked for
+    int seg = 0, stop = 0;        // segments whose queries, parts of tile n that were asked for
+#pragma unroll 1
     for (; ok && w.next(seg == 0); ++seg) {
-      if (seg > 0) ok = warp_wait(q_empty, (seg - 1) & 1, P.err);
+      if (warp == 0 && seg > 0) ok = all_wait(q_empty, (seg - 1) & 1, P.err);
       if (!ok) break;
-      if (lane == 0) {
+      if (warp == 0 && lane == 0) {
         mbar_arrive_expect_tx(q_full, kChunks * static_cast<uint32_t>(heads) * 128);
+#pragma unroll 1
         for (int c = 0; c < kChunks; ++c)
           tma_load_2d(sbase + kOffQ + c * kQChunk, &tq, 64 * c, w.b * P.H + g * kHeads, q_full);
       }
       Box x = box_of(P.c, w.k, w.b, w.k.tile(w.i0), lane, P.err);
+#pragma unroll 1
       for (int i = w.i0; i < w.i1; ++i, ++n) {
         Box nx;                   // the next tile's page ids, fetched a tile ahead
         nx.on = false;
-        if (i + 1 < w.i1) nx = box_of(P.c, w.k, w.b, w.k.tile(i + 1), lane, P.err);
+        if (i + 1 < w.i1) {
+          nx = box_of(P.c, w.k, w.b, w.k.tile(i + 1), lane, P.err);
+          if (warp == kLoaders - 1) prefetch_box(P.c, nx);
+        }
         const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, x.on));
         const uint32_t dst = sbase + kOffX + static_cast<uint32_t>(lane * P.c.box) * 128;
-        for (int c = 0; c < kChunks; ++c) {
-          ok = warp_wait(empty(c), (n & 1) ^ 1, P.err);
+#pragma unroll 1
+        for (int c = warp; c < kParts; c += kLoaders) {
+          ok = all_wait(empty(c), (n & 1) ^ 1, P.err);
           if (!ok) {
             stop = c;
             break;
           }
-          if (lane == 0) mbar_arrive_expect_tx(full(c), boxes * static_cast<uint32_t>(P.c.box) * 128);
+          const uint32_t cols = c < 4 ? 2u : 1u;
+          if (lane == 0)
+            mbar_arrive_expect_tx(full(c), boxes * cols * static_cast<uint32_t>(P.c.box) * 128);
           __syncwarp();
-          if (x.on) tma_load_3d(dst + c * kChunkBytes, &tx, 64 * c, x.row, x.page, full(c));
+          if (x.on)
+#pragma unroll 1
+            for (uint32_t u = 0; u < cols; ++u)
+              tma_load_3d(dst + (2 * c + u) * kChunkBytes, &tx, 64 * (2 * c + u), x.row, x.page,
+                          full(c));
         }
         if (!ok) break;
         x = nx;
@@ -188,173 +208,201 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // after a failure, let the copies in flight land before the memory goes
     if (!ok && lane == 0) {
-      if (seg > 0) mbar_wait_drain(q_full, (seg - 1) & 1, P.err);
-      for (int c = 0; c < kChunks; ++c) {
+      if (warp == 0 && seg > 0) mbar_wait_drain(q_full, (seg - 1) & 1, P.err);
+#pragma unroll 1
+      for (int c = warp; c < kParts; c += kLoaders) {
         const uint32_t asked = n + (c < stop ? 1 : 0);
         if (asked > 0) mbar_wait_drain(full(c), (asked - 1) & 1, P.err);
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp == kLoaders) {
     // ------------------------------------------------------------ MMA
-    if (lane == 0) {
-      const uint64_t dXk = smem_desc(sbase + kOffX, 16, 1024, kSwizzle128B);
-      const uint64_t dQ = smem_desc(sbase + kOffQ, 16, 1024, kSwizzle128B);
-      const uint64_t dXv = smem_desc(sbase + kOffX, kChunkBytes, 1024, kSwizzle128B);
-      const uint64_t dP = smem_desc(sbase + kOffP, kChunkBytes, 1024, kSwizzle128B);
-      uint32_t n = 0;
-      bool ok = true;
-      for (int seg = 0; ok && w.next(seg == 0); ++seg) {
-        ok = mbar_wait(q_full, seg & 1, P.err);
-        for (int i = w.i0; ok && i < w.i1; ++i, ++n) {
+    // The whole warp walks the tiles and one elected lane issues each run of
+    // MMAs: every operand stays warp-uniform.  (Issued from a one-lane branch an
+    // MMA took about 90 cycles to issue, twice its own time.)
+    const uint64_t dXk = smem_desc(sbase + kOffX, 16, 1024, kSwizzle128B);
+    const uint64_t dQ = smem_desc(sbase + kOffQ, 16, 1024, kSwizzle128B);
+    const uint64_t dXv = smem_desc(sbase + kOffX, kChunkBytes, 1024, kSwizzle128B);
+    const uint64_t dP = smem_desc(sbase + kOffP, kChunkBytes, 1024, kSwizzle128B);
+    uint32_t n = 0;
+    bool ok = true;
+    for (int seg = 0; ok && w.next(seg == 0); ++seg) {
+      ok = all_wait(q_full, seg & 1, P.err);
 #pragma unroll 1
-          for (int c = 0; ok && c < kChunks; ++c) {
-            ok = mbar_wait(full(c), n & 1, P.err);
-            if (!ok) break;
-            tc_fence_after();
+      for (int i = w.i0; ok && i < w.i1; ++i, ++n) {
+        const bool last = i + 1 == w.i1;
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_f16(tmem + kColS, dXk + ((c * kChunkBytes + kk * 32) >> 4),
-                      dQ + ((c * kQChunk + kk * 32) >> 4), kIdescS, (c | kk) != 0 ? 1u : 0u);
-          }
-          if (!ok) break;
-          mma_commit(s_full);
-          if (i + 1 == w.i1) mma_commit(q_empty);
-          // the last segment's O^T must have been read out
-          if (i == w.i0 && seg > 0) ok = mbar_wait(o_empty, (seg - 1) & 1, P.err);
-          ok = ok && mbar_wait(p_full, n & 1, P.err);
+        for (int c = 0; c < 8; c += 4) {
+          ok = ok && all_wait(full(c / 2), n & 1, P.err);
           if (!ok) break;
           tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < 16; ++kk)
+              mma_f16(tmem + kColS, dXk + (((c + kk / 4) * kChunkBytes + (kk % 4) * 32) >> 4),
+                      dQ + (((c + kk / 4) * kQChunk + (kk % 4) * 32) >> 4), kIdescS,
+                      c + kk > 0 ? 1u : 0u);
+          }
+          __syncwarp();
+        }
+        ok = ok && all_wait(full(4), n & 1, P.err);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f16(tmem + kColS, dXk + ((8 * kChunkBytes + kk * 32) >> 4),
+                    dQ + ((8 * kQChunk + kk * 32) >> 4), kIdescS, 1u);
+          mma_commit(s_full);
+          if (last) mma_commit(q_empty);
+        }
+        __syncwarp();
+        // the last segment's O^T must have been read out
+        if (ok && i == w.i0 && seg > 0) ok = all_wait(o_empty, (seg - 1) & 1, P.err);
+        ok = ok && all_wait(p_full, n & 1, P.err);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t more = i > w.i0 ? 1u : 0u;
 #pragma unroll 1
           for (int mt = 0; mt < 4; ++mt) {
 #pragma unroll
             for (int kk = 0; kk < kTile / 16; ++kk)
               mma_f16(tmem + kColO + 64u * mt, dXv + ((mt * 2 * kChunkBytes + kk * 2048) >> 4),
-                      dP + ((kk * 2048) >> 4), kIdescO, (i > w.i0 || kk > 0) ? 1u : 0u);
-            mma_commit(empty(2 * mt));
-            mma_commit(empty(2 * mt + 1));
+                      dP + ((kk * 2048) >> 4), kIdescO, kk > 0 ? 1u : more);
+            mma_commit(empty(mt));
           }
-          mma_commit(empty(8));
-          if (i + 1 == w.i1) mma_commit(o_full);
+          mma_commit(empty(4));
+          if (last) mma_commit(o_full);
         }
+        __syncwarp();
       }
-      mma_commit(drain);
-      mbar_wait_drain(drain, 0, P.err);
     }
+    mma_commit_warp(drain);
+    if (lane == 0) mbar_wait_drain(drain, 0, P.err);
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax
-    // Two warpgroups; a thread owns one key of the tile (TMEM lane) and 32 of
-    // the heads.
-    const int wg = (warp - 2) >> 2;
+    // Four warpgroups; a thread owns one key of the tile (TMEM lane) and 16 of
+    // the heads.  (Two warpgroups of 32 heads a thread took 1.5 times as long over
+    // a tile: too few warps to cover each other's latencies.)
+    const int wg = (warp - kLoaders - 1) >> 2;
     const int sp = warp & 3;                          // TMEM sub-partition
     const int r = sp * 32 + lane;                     // key in the tile
-    const int tid = threadIdx.x - 64;                 // 0..255
+    const int tid = threadIdx.x - 32 * (kLoaders + 1);                 // 0..511
     const uint32_t lane_base = static_cast<uint32_t>(sp * 32) << 16;
-    const int h0 = 32 * wg;
+    const int h0 = kWide * wg;
     uint8_t* prow = smem + kOffP + r * 128;
     uint32_t n = 0;
     bool ok = true;
     for (int seg = 0; ok && w.next(seg == 0); ++seg) {
-      float2 l[16], lr[16];       // sums of P and of P as rounded to bf16
+      float2 l[kWide / 2];               // sums of P
 #pragma unroll
-      for (int e = 0; e < 16; ++e) l[e] = lr[e] = make_float2(0.f, 0.f);
+      for (int e = 0; e < kWide / 2; ++e) l[e] = make_float2(0.f, 0.f);
+#pragma unroll 1
       for (int i = w.i0; i < w.i1; ++i, ++n) {
-        const int tile = w.k.tile(i);
-        const bool seen = w.k.key(tile * kTile + r);
-        const bool bad = !warp_wait(s_full, n & 1, P.err);
-        uint32_t v[32];
+        const bool seen = w.k.key(w.k.tile(i) * kTile + r);
+        const bool bad = !all_wait(s_full, n & 1, P.err);
+        const float2 sc = make_float2(P.scale_log2, P.scale_log2);
+        float2 y[kWide / 2];             // scores over the references, log2 units
+        auto load = [&]() {
+          uint32_t v[kWide];
+          tmem_ld_x16(tmem + lane_base + kColS + h0, v);
+          tmem_wait_ld();
+          if (!seen)
+#pragma unroll
+            for (int e = 0; e < kWide; ++e) v[e] = 0xff800000u;
+#pragma unroll
+          for (int e = 0; e < kWide / 2; ++e)
+            y[e] = make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+        };
+        auto shift = [&]() {
+#pragma unroll
+          for (int e = 0; e < kWide / 2; e += 2) {
+            const float4 m = *reinterpret_cast<const float4*>(ref + h0 + 2 * e);
+            y[e] = __ffma2_rn(y[e], sc, make_float2(m.x, m.y));
+            y[e + 1] = __ffma2_rn(y[e + 1], sc, make_float2(m.z, m.w));
+          }
+        };
         bool over = false;
         if (!bad) {
           tc_fence_after();
-          tmem_ld_32x32b_x32(tmem + lane_base + kColS + h0, v);
-          tmem_wait_ld();
-          tc_fence_before();
-        }
-        if (!seen)
+          load();
+          if (i > w.i0) {
+            shift();
+            float top = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = 0xff800000u;
-        const float2 sc = make_float2(P.scale_log2, P.scale_log2);
-        if (i > w.i0) {
-          float top = -INFINITY;
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 m = *reinterpret_cast<const float4*>(ref + h0 + e);
-            top = fmaxf(top, __uint_as_float(v[e]) * P.scale_log2 - m.x);
-            top = fmaxf(top, __uint_as_float(v[e + 1]) * P.scale_log2 - m.y);
-            top = fmaxf(top, __uint_as_float(v[e + 2]) * P.scale_log2 - m.z);
-            top = fmaxf(top, __uint_as_float(v[e + 3]) * P.scale_log2 - m.w);
+            for (int e = 0; e < kWide / 2; ++e) top = max3(top, y[e].x, y[e].y);
+            over = top > kSlack;
           }
-          over = top > kSlack;
         }
-        // one vote for all eight warps; it also takes them out together when
+        // the weights, in the hope that the references stand
+        uint32_t pk[kWide / 2];
+        auto weigh = [&]() {
+#pragma unroll
+          for (int e = 0; e < kWide / 2; ++e) {
+            y[e] = make_float2(fast_exp2(y[e].x), fast_exp2(y[e].y));
+            pk[e] = pack_bf16x2(y[e].x, y[e].y);
+          }
+        };
+        if (i > w.i0) weigh();
+        // one vote for all the warps; it also takes them out together when
         // a wait of one of them gave up
-        if (named_bar_or(1, 256, bad || over) || i == w.i0) {
-          if (named_bar_or(1, 256, bad)) {
+        if (named_bar_or(1, kSoftThreads, bad || over) || i == w.i0) {
+          if (named_bar_or(1, kSoftThreads, bad)) {
             ok = false;
             break;
           }
           // new references: the columns' maxima over the tile
-          float m[32];
+          if (i > w.i0) load();
+          float m[kWide];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) m[e] = __uint_as_float(v[e]) * P.scale_log2;
-          red[sp * kHeads + h0 + lane] = column_reduce<true>(m);
-          named_bar_sync(1, 256);
+          for (int e = 0; e < kWide / 2; ++e) {
+            m[2 * e] = y[e].x * P.scale_log2;
+            m[2 * e + 1] = y[e].y * P.scale_log2;
+          }
+          const float top = column_reduce<true>(m);
+          if (lane < kWide) red[sp * kHeads + h0 + lane] = top;
+          named_bar_sync(1, kSoftThreads);
           if (tid < kHeads) {
-            const float old = i > w.i0 ? ref[tid] : kNoRef;
+            const float old = i > w.i0 ? -ref[tid] : kNoRef;
             const float top = fmaxf(fmaxf(red[tid], red[kHeads + tid]),
                                     fmaxf(red[2 * kHeads + tid], red[3 * kHeads + tid]));
             const float now = fmaxf(old, top);
             alpha[tid] = fast_exp2(old - now);
-            ref[tid] = now;
+            ref[tid] = -now;
           }
-          named_bar_sync(1, 256);
+          named_bar_sync(1, kSoftThreads);
           if (i > w.i0) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float2 al = *reinterpret_cast<const float2*>(alpha + h0 + 2 * e);
-              l[e] = __fmul2_rn(l[e], al);
-              lr[e] = __fmul2_rn(lr[e], al);
-            }
+            for (int e = 0; e < kWide / 2; ++e)
+              l[e] = __fmul2_rn(l[e], *reinterpret_cast<const float2*>(alpha + h0 + 2 * e));
             // every earlier product is complete: this tile's last chunk could
             // only be loaded after it
 #pragma unroll 1
             for (int mt = 0; mt < 4; ++mt) {
-              uint32_t o[32];
-              tmem_ld_32x32b_x32(tmem + lane_base + kColO + 64u * mt + h0, o);
+              uint32_t o[kWide];
+              tmem_ld_x16(tmem + lane_base + kColO + 64u * mt + h0, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha[h0 + e]);
-              tmem_st_32x32b_x32(tmem + lane_base + kColO + 64u * mt + h0, o);
+              for (int e = 0; e < kWide; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha[h0 + e]);
+              tmem_st_x16(tmem + lane_base + kColO + 64u * mt + h0, o);
             }
             tmem_wait_st();
           }
+          shift();
+          weigh();
         }
 #pragma unroll
-        for (int e = 0; e < 32; e += 8) {
-          uint32_t pk[4];
-#pragma unroll
-          for (int u = 0; u < 8; u += 2) {
-            const float2 m = *reinterpret_cast<const float2*>(ref + h0 + e + u);
-            const float2 y = __ffma2_rn(make_float2(__uint_as_float(v[e + u]),
-                                                    __uint_as_float(v[e + u + 1])),
-                                        sc, make_float2(-m.x, -m.y));
-            const float2 p = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-            const int a = (e + u) / 2;
-            l[a] = __fadd2_rn(l[a], p);
-            const uint32_t b = pack_bf16x2(p.x, p.y);
-            pk[u / 2] = b;
-            lr[a] = __fadd2_rn(lr[a], make_float2(__uint_as_float(b << 16),
-                                                  __uint_as_float(b & 0xFFFF0000u)));
-          }
-          *reinterpret_cast<uint4*>(prow + (((h0 + e) / 8) ^ (r & 7)) * 16) =
-              make_uint4(pk[0], pk[1], pk[2], pk[3]);
-        }
+        for (int e = 0; e < kWide / 2; e += 4)
+          *reinterpret_cast<uint4*>(prow + ((h0 / 8 + e / 4) ^ (r & 7)) * 16) =
+              make_uint4(pk[e], pk[e + 1], pk[e + 2], pk[e + 3]);
         // an unseen row of the tile holds whatever its memory held: its
         // weight is 0, and so must its value be (0 * NaN is not)
         if (!seen) {
 #pragma unroll 1
-          for (int c = 4 * wg; c < 4 * wg + 4; ++c)
+          for (int c = 2 * wg; c < 2 * wg + 2; ++c)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
               *reinterpret_cast<uint4*>(smem + kOffX + c * kChunkBytes + r * 128 + (j ^ (r & 7)) * 16) =
@@ -364,21 +412,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full);
+#pragma unroll
+        for (int e = 0; e < kWide / 2; ++e) l[e] = __fadd2_rn(l[e], y[e]);
       }
       if (!ok) break;
       // ---------------------------------------------------------- read-out
-      float ls[32], ls2[32];
+      float ls[kWide];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
+      for (int e = 0; e < kWide / 2; ++e) {
         ls[2 * e] = l[e].x;
         ls[2 * e + 1] = l[e].y;
-        ls2[2 * e] = lr[e].x;
-        ls2[2 * e + 1] = lr[e].y;
       }
-      red[sp * kHeads + h0 + lane] = column_reduce<false>(ls);
-      red[4 * kHeads + sp * kHeads + h0 + lane] = column_reduce<false>(ls2);
-      const bool bad = !warp_wait(o_full, seg & 1, P.err);
-      if (named_bar_or(1, 256, bad)) {
+      const float part = column_reduce<false>(ls);
+      if (lane < kWide) red[sp * kHeads + h0 + lane] = part;
+      const bool bad = !all_wait(o_full, seg & 1, P.err);
+      if (named_bar_or(1, kSoftThreads, bad)) {
         ok = false;
         break;
       }
@@ -387,27 +435,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = w.i0 == 0 && w.i1 == tiles;
       const int64_t slot = (static_cast<int64_t>(piece) * 2 + (seg == 0 ? 0 : 1)) * P.groups + g;
       if (tid < heads) {
-        float sum = 0.f, sumr = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          sum += red[e * kHeads + tid];
-          sumr += red[(4 + e) * kHeads + tid];
-        }
+        const float sum = (red[tid] + red[kHeads + tid]) + (red[2 * kHeads + tid] + red[3 * kHeads + tid]);
         const int64_t at = static_cast<int64_t>(w.b) * P.H + g * kHeads + tid;
         if (whole) {
-          if (P.lse) P.lse[at] = sum == 0.f ? -INFINITY : (ref[tid] + log2f(sum)) * kLn2;
+          if (P.lse) P.lse[at] = sum == 0.f ? -INFINITY : (log2f(sum) - ref[tid]) * kLn2;
         } else {
-          P.ml[slot * kHeads + tid] = make_float4(ref[tid], sum, sumr, 0.f);
+          P.ml[slot * kHeads + tid] = make_float2(-ref[tid], sum);
         }
-        alpha[tid] = sumr == 0.f ? 0.f : 1.f / sumr;
+        alpha[tid] = sum == 0.f ? 0.f : 1.f / sum;
       }
       if (w.i0 == 0 && g == 0 && tid == 0)
         P.plan[w.b] = piece * start.per + start.per - w.left - (w.i1 - w.i0);
-      named_bar_sync(1, 256);
+      named_bar_sync(1, kSoftThreads);
 #pragma unroll 1
       for (int mt = 0; mt < 4; ++mt) {
-        uint32_t o[32];
-        tmem_ld_32x32b_x32(tmem + lane_base + kColO + 64u * mt + h0, o);
+        uint32_t o[kWide];
+        tmem_ld_x16(tmem + lane_base + kColO + 64u * mt + h0, o);
         tmem_wait_ld();
         if (whole) {
           // lanes hold neighbouring dims: pairs of lanes swap so that each
@@ -415,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int d = mt * 128 + sp * 32 + (lane & ~1);
           __nv_bfloat16* dst = P.out + (static_cast<int64_t>(w.b) * P.H + g * kHeads + h0) * kDv + d;
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
+          for (int e = 0; e < kWide; e += 2) {
             const float2 iv = *reinterpret_cast<const float2*>(alpha + h0 + e);
             const float a = __uint_as_float(o[e]) * iv.x, b = __uint_as_float(o[e + 1]) * iv.y;
             const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? a : b, 1);
@@ -427,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           float* dst = P.part + (slot * kHeads + h0) * kDv + mt * 128 + r;
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
+          for (int e = 0; e < kWide; ++e)
             if (h0 + e < heads) dst[e * kDv] = __uint_as_float(o[e]);
         }
       }
@@ -435,13 +478,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(o_empty);
       // the references and sums are read above; the next segment rewrites them
-      named_bar_sync(1, 256);
+      named_bar_sync(1, kSoftThreads);
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == kLoaders) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -469,28 +512,26 @@ __global__ void __launch_bounds__(128) combine_kernel(const Params P) {
   };
   if (threadIdx.x < 32) {
     float top = -INFINITY;
+#pragma unroll 1
     for (int i = threadIdx.x; i < parts; i += 32) {
-      const float4 x = P.ml[slot(i) * kHeads + hh];
+      const float2 x = P.ml[slot(i) * kHeads + hh];
       if (x.y != 0.f) top = fmaxf(top, x.x);          // a part without a weight has no reference
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    float l = 0.f, lr = 0.f;
+    float l = 0.f;
+#pragma unroll 1
     for (int i = threadIdx.x; i < parts; i += 32) {
-      const float4 x = P.ml[slot(i) * kHeads + hh];
+      const float2 x = P.ml[slot(i) * kHeads + hh];
       const float f = x.y != 0.f ? exp2f(x.x - top) : 0.f;
       wt[i] = f;
       l += f * x.y;
-      lr += f * x.z;
     }
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-      l += __shfl_xor_sync(0xffffffffu, l, d);
-      lr += __shfl_xor_sync(0xffffffffu, lr, d);
-    }
+    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
     if (threadIdx.x == 0) {
       tot[0] = l;
-      tot[1] = lr == 0.f ? 0.f : 1.f / lr;
+      tot[1] = l == 0.f ? 0.f : 1.f / l;
       tot[2] = top;
     }
   }
@@ -532,7 +573,7 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 size_t paged_decode_workspace_bytes(int B, int H, int max_len_k) {
   const size_t slots = static_cast<size_t>(2) * pieces_of(B, H, max_len_k) * groups_of(H);
-  return up256((static_cast<size_t>(B) + 1) * 4) + slots * kHeads * (16 + kDv * 4);
+  return up256((static_cast<size_t>(B) + 1) * 4) + slots * kHeads * (8 + kDv * 4);
 }
 
 cudaError_t launch_paged_decode(const CUtensorMap& tq, const CUtensorMap& tx,
@@ -548,8 +589,8 @@ cudaError_t launch_paged_decode(const CUtensorMap& tq, const CUtensorMap& tx,
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   P.plan = reinterpret_cast<int32_t*>(ws);
   ws += up256((static_cast<size_t>(a.cache.B) + 1) * 4);
-  P.ml = reinterpret_cast<float4*>(ws);
-  ws += static_cast<size_t>(2) * P.pieces * P.groups * kHeads * 16;
+  P.ml = reinterpret_cast<float2*>(ws);
+  ws += static_cast<size_t>(2) * P.pieces * P.groups * kHeads * 8;
   P.part = reinterpret_cast<float*>(ws);
   P.err = err;
   cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel,
