@@ -449,6 +449,34 @@ DSA_API dsa_status_t dsa_paged_mla_decode(const void* q, const void* kv_cache, i
  * are split over the GPU.  Returns 0 for invalid sizes. */
 DSA_API size_t dsa_paged_mla_decode_workspace_size(int B, int H, int max_len_k);
 
+/*
+ * The attention weight each cached entry got from its sequence's newest token,
+ * summed over the heads and added to a running total (what a cache is cut
+ * down by, see dsa_cache_evict):
+ *
+ *   mass_out[b, s] = mass_in[b, s] + sum_h exp(sm_scale * q[b,h,:] . x[s] - lse[b,h])
+ *
+ * for the entries s the token sees; for the other entries below the
+ * sequence's length, mass_out[b, s] = mass_in[b, s].  Entries at or past the
+ * length are left untouched.
+ *
+ *  q, kv_cache, block_table, seq_lens, window, sinks, sm_scale: as given to
+ *           dsa_paged_mla_decode
+ *  lse      (device) f32 [B, H], as that call wrote it
+ *  mass_in  (device, nullable) f32, row b at mass_in + b * ld_mass; NULL reads
+ *           as zeros; may be mass_out itself (and must not overlap it otherwise)
+ *  mass_out (device) f32, row b at mass_out + b * ld_mass, ld_mass >= max_len_k
+ *  Supported: d_qk = 576, H as for dsa_paged_mla_decode.
+ *  Arithmetic: bf16 tensor-core products, fp32 sums.
+ */
+DSA_API dsa_status_t dsa_paged_attn_mass(const void* q, const void* kv_cache, int64_t n_pages,
+                                         int page_size, int64_t page_stride,
+                                         const int32_t* block_table, int64_t block_table_ld,
+                                         int max_pages, const int32_t* seq_lens, int B,
+                                         int max_len_k, int H, int d_qk, int window, int sinks,
+                                         float sm_scale, const float* lse, const float* mass_in,
+                                         float* mass_out, int64_t ld_mass, void* stream);
+
 /* Bytes of workspace dsa_forward needs: an f32 score matrix [total_q,
  * round_up(max_len_k, 4)] plus an int32 index matrix [total_q, k], each
  * 256-byte aligned.  Returns 0 for invalid sizes. */

@@ -19,7 +19,7 @@ __all__ = [
     "dsa_indexer_kl_workspace_size", "dsa_masked_mha_fwd", "dsa_masked_mha_workspace_size",
     "dsa_debug_fault_injection", "dsa_indexer_backward", "dsa_forward_fused",
     "dsa_forward_fused_workspace_size", "dsa_paged_mla_decode",
-    "dsa_paged_mla_decode_workspace_size", "EXPORTED",
+    "dsa_paged_mla_decode_workspace_size", "dsa_paged_attn_mass", "EXPORTED",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -34,7 +34,7 @@ EXPORTED = (
     "dsa_indexer_kl", "dsa_indexer_kl_workspace_size", "dsa_masked_mha_fwd",
     "dsa_masked_mha_workspace_size", "dsa_debug_fault_injection", "dsa_indexer_backward",
     "dsa_forward_fused", "dsa_forward_fused_workspace_size", "dsa_paged_mla_decode",
-    "dsa_paged_mla_decode_workspace_size",
+    "dsa_paged_mla_decode_workspace_size", "dsa_paged_attn_mass",
 )
 
 STATUS = {
@@ -105,6 +105,9 @@ def load():
     lib.dsa_paged_mla_decode.restype = I
     lib.dsa_paged_mla_decode_workspace_size.argtypes = [I, I, I]
     lib.dsa_paged_mla_decode_workspace_size.restype = ctypes.c_size_t
+    lib.dsa_paged_attn_mass.argtypes = [P, P, I64, I, I64, P, I64, I, P, I, I, I, I, I, I, F, P, P,
+                                        P, I64, P]
+    lib.dsa_paged_attn_mass.restype = I
     lib.dsa_debug_fault_injection.argtypes = [ctypes.c_uint64, I]
     lib.dsa_debug_fault_injection.restype = None
     lib.dsa_version.argtypes = []
@@ -532,6 +535,42 @@ def dsa_paged_mla_decode(q, kv_cache, block_table, seq_lens, max_len_k, sm_scale
             int(sinks), float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace),
             int(workspace.numel()), ctypes.c_void_p(st.cuda_stream))
     _check(rc, "dsa_paged_mla_decode")
+
+
+def _rows_f32(t, B, n, name):
+    """A CUDA float32 matrix [B, >= n] with contiguous rows; its row stride."""
+    import torch
+    if t.dtype != torch.float32 or not t.is_cuda or t.dim() != 2 or t.shape[0] != B:
+        raise ValueError(f"{name} must be a CUDA torch.float32 tensor [B, entries]")
+    if t.shape[1] < n or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must have contiguous rows of at least {n} entries")
+    return int(t.stride(0)) if B > 1 else int(t.shape[1])
+
+
+def dsa_paged_attn_mass(q, kv_cache, block_table, seq_lens, lse, max_len_k, sm_scale, mass_out,
+                        mass_in=None, window=0, sinks=0, stream=None):
+    """Adds to mass_in [B, >= max_len_k] (None: zeros) the attention weight each
+    cached entry got from the newest token, summed over the heads, into mass_out
+    (which may be mass_in); lse as dsa_paged_mla_decode wrote it for the same
+    arguments (see include/dsa.h)."""
+    import torch
+    _need(q, torch.bfloat16, "q", 3)
+    _need(lse, torch.float32, "lse", 2)
+    cache = _paged(kv_cache, block_table, seq_lens, q=q, lse=lse, mass_out=mass_out,
+                   mass_in=mass_in)
+    B, H, d_qk = q.shape
+    _shape(q, (seq_lens.shape[0], H, d_qk), "q")
+    _shape(lse, (B, H), "lse")
+    ld = _rows_f32(mass_out, B, int(max_len_k), "mass_out")
+    if mass_in is not None and _rows_f32(mass_in, B, int(max_len_k), "mass_in") != ld and B > 1:
+        raise ValueError("mass_in and mass_out must have the same row stride")
+    st = _stream_on(stream, q.device)
+    with torch.cuda.device(q.device):
+        rc = load().dsa_paged_attn_mass(
+            _ptr(q), *cache, int(max_len_k), int(H), int(d_qk), int(window), int(sinks),
+            float(sm_scale), _ptr(lse), _ptr(mass_in), _ptr(mass_out), ld,
+            ctypes.c_void_p(st.cuda_stream))
+    _check(rc, "dsa_paged_attn_mass")
 
 
 def dsa_get_device_error(stream=None) -> int:

@@ -772,6 +772,52 @@ dsa_status_t dsa_paged_mla_decode(const void* q, const void* kv_cache, int64_t n
       dsa::launch_paged_decode(tq, tx, a, next_err(dev), static_cast<cudaStream_t>(stream)));
 }
 
+dsa_status_t dsa_paged_attn_mass(const void* q, const void* kv_cache, int64_t n_pages,
+                                 int page_size, int64_t page_stride, const int32_t* block_table,
+                                 int64_t block_table_ld, int max_pages, const int32_t* seq_lens,
+                                 int B, int max_len_k, int H, int d_qk, int window, int sinks,
+                                 float sm_scale, const float* lse, const float* mass_in,
+                                 float* mass_out, int64_t ld_mass, void* stream) {
+  if (!q || !lse || !mass_out || window < 0 || sinks < 0) return DSA_ERR_INVALID_ARG;
+  if (d_qk != 576 || !mla_heads_ok(H)) return DSA_ERR_UNSUPPORTED;
+  dsa_status_t st = check_cache(kv_cache, n_pages, page_size, page_stride, block_table,
+                                block_table_ld, max_pages, seq_lens, B, max_len_k);
+  if (st != DSA_OK) return st;
+  if (!(sm_scale > 0.f) || sm_scale != sm_scale) return DSA_ERR_INVALID_ARG;
+  if (ld_mass < max_len_k) return DSA_ERR_INVALID_ARG;
+  if (!aligned16(q)) return DSA_ERR_ALIGNMENT;
+  if (static_cast<int64_t>(B) * H >= (int64_t(1) << 31)) return DSA_ERR_UNSUPPORTED;
+  if (B == 0 || max_len_k == 0) return DSA_OK;
+  DeviceInfo* dev = nullptr;
+  if ((st = device_info(&dev)) != DSA_OK) return st;
+  dsa::PagedMassArgs a;
+  a.cache = cache_of(kv_cache, n_pages, page_size, page_stride, block_table, block_table_ld,
+                     max_pages, seq_lens, B, max_len_k, window, sinks);
+  a.H = H;
+  a.max_len_k = max_len_k;
+  a.sm_scale = sm_scale;
+  a.lse = lse;
+  a.in = mass_in;
+  a.out = mass_out;
+  a.ld = ld_mass;
+  a.num_sms = dev->num_sms;
+  CUtensorMap tq[2], tx;
+  dsa::DevErr err[2];
+  const int launches = (H + 127) / 128;
+  for (int i = 0; i < launches; ++i) {
+    const int heads = H - 128 * i < 128 ? H - 128 * i : 128;
+    if ((st = encode_2d(&tq[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q,
+                        static_cast<uint64_t>(B) * H, 576, 2, static_cast<uint32_t>(heads), 64,
+                        CU_TENSOR_MAP_SWIZZLE_128B)) != DSA_OK)
+      return st;
+    err[i] = next_err(dev);
+  }
+  if ((st = encode_pool(&tx, kv_cache, n_pages, page_size, page_stride, a.cache.box)) != DSA_OK)
+    return st;
+  return from_cuda(
+      dsa::launch_paged_mass(tq, launches, tx, a, err, static_cast<cudaStream_t>(stream)));
+}
+
 void dsa_debug_fault_injection(uint64_t wait_limit_ns, int drop_first_key_load) {
   g_wait_limit_ns.store(wait_limit_ns);
   g_inject_indexer.store(drop_first_key_load ? dsa::kInjectDropFirstKeyLoad : 0u);

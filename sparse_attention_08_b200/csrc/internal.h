@@ -195,4 +195,18 @@ cudaError_t launch_paged_decode(const CUtensorMap& tq, const CUtensorMap& tx,
                                 const PagedDecodeArgs& a, DevErr err, cudaStream_t s);
 size_t paged_decode_workspace_bytes(int B, int H, int max_len_k);
 
+struct PagedMassArgs {
+  paged::Cache cache;
+  int H, max_len_k;
+  float sm_scale;
+  const float* lse;
+  const float* in;   // nullable
+  float* out;
+  int64_t ld;
+  int num_sms;
+};
+// One launch per 128 heads, with its own query map and error record.
+cudaError_t launch_paged_mass(const CUtensorMap* tq, int launches, const CUtensorMap& tx,
+                              const PagedMassArgs& a, const DevErr* err, cudaStream_t s);
+
 }  // namespace dsa

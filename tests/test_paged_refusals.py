@@ -69,3 +69,22 @@ def test_wrappers_check_tensors():
                                  t((2, 16, 576), dtype=torch.bfloat16),
                                  t((1, 2), dtype=torch.int32), t(1, dtype=torch.int32), 32, 0.04,
                                  t((1, 16, 512), dtype=torch.bfloat16))
+
+
+def mass(**kw):
+    a = dict(CACHE, q=P, H=128, d_qk=576, window=0, sinks=0, scale=0.04, lse=P, m_in=P, m_out=P,
+             ld_m=640)
+    a.update(kw)
+    return dsa.load().dsa_paged_attn_mass(a["q"], *cache_args(a), a["H"], a["d_qk"], a["window"],
+                                          a["sinks"], a["scale"], a["lse"], a["m_in"], a["m_out"],
+                                          a["ld_m"], None)
+
+
+@pytest.mark.parametrize("kw,status", BAD_CACHE + [
+    (dict(q=None), INVALID), (dict(lse=None), INVALID), (dict(m_out=None), INVALID),
+    (dict(window=-1), INVALID), (dict(sinks=-1), INVALID), (dict(scale=-1.0), INVALID),
+    (dict(ld_m=639), INVALID), (dict(H=100), UNSUPPORTED), (dict(d_qk=512), UNSUPPORTED),
+    (dict(q=off(2)), ALIGN), (dict(B=0), OK), (dict(max_len=0), OK),
+])
+def test_mass_refuses(kw, status):
+    assert mass(**kw) == status
