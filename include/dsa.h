@@ -477,6 +477,44 @@ DSA_API dsa_status_t dsa_paged_attn_mass(const void* q, const void* kv_cache, in
                                          float sm_scale, const float* lse, const float* mass_in,
                                          float* mass_out, int64_t ld_mass, void* stream);
 
+/*
+ * Cuts the sequences of a cache down to at most `budget` entries by a running
+ * total per entry (dsa_paged_attn_mass's).  A sequence of n <= budget entries
+ * keeps them all; a longer one keeps its first `sinks`, its last `recent`, and
+ * of those between the budget - sinks - recent with the largest totals, ties to
+ * the lower position.  The kept latents are copied, in their order, to the
+ * pages that new_block_table names: kept entry j goes to row j % page_size of
+ * page new_block_table[b, j / page_size].  The old pages are left as they are.
+ *
+ *  kv_cache, block_table, seq_lens, max_len_k: as for dsa_paged_mla_decode; the
+ *           new pages lie in the same pool
+ *  mass     (device) f32, row b at mass + b * ld_mass (ld_mass >= max_len_k);
+ *           NaN counts as larger than every number, -0 equals +0
+ *  new_block_table (device) int32, new_max_pages entries in row b at
+ *           new_block_table + b * new_block_table_ld; covers
+ *           min(budget, max_len_k) entries.  Its pages must be different from
+ *           one another and from every page that a sequence of the call
+ *           still reads (the copies run in no order).
+ *  new_lens (device) int32 [B]: min(n, budget); not seq_lens itself
+ *  idx_out  (device) int32 [B, budget]: the kept entries' old positions,
+ *           ascending, padded with -1 (to cut other per-entry data alike)
+ *  new_mass (device, nullable) f32, row b at new_mass + b * ld_new_mass
+ *           (ld_new_mass >= budget): the kept entries' totals, padded with 0
+ *           up to `budget`; not mass itself
+ *  Supported: max_len_k <= 262144, sinks + recent <= budget.
+ *  A page id outside the pool, in either table, sets DSA_ERR_BOUNDS and that
+ *  entry's latent is not copied.
+ */
+DSA_API dsa_status_t dsa_cache_evict(void* kv_cache, int64_t n_pages, int page_size,
+                                     int64_t page_stride, const int32_t* block_table,
+                                     int64_t block_table_ld, int max_pages,
+                                     const int32_t* seq_lens, int B, int max_len_k,
+                                     const float* mass, int64_t ld_mass, int budget, int sinks,
+                                     int recent, const int32_t* new_block_table,
+                                     int64_t new_block_table_ld, int new_max_pages,
+                                     int32_t* new_lens, int32_t* idx_out, float* new_mass,
+                                     int64_t ld_new_mass, void* stream);
+
 /* Bytes of workspace dsa_forward needs: an f32 score matrix [total_q,
  * round_up(max_len_k, 4)] plus an int32 index matrix [total_q, k], each
  * 256-byte aligned.  Returns 0 for invalid sizes. */

@@ -19,7 +19,8 @@ __all__ = [
     "dsa_indexer_kl_workspace_size", "dsa_masked_mha_fwd", "dsa_masked_mha_workspace_size",
     "dsa_debug_fault_injection", "dsa_indexer_backward", "dsa_forward_fused",
     "dsa_forward_fused_workspace_size", "dsa_paged_mla_decode",
-    "dsa_paged_mla_decode_workspace_size", "dsa_paged_attn_mass", "EXPORTED",
+    "dsa_paged_mla_decode_workspace_size", "dsa_paged_attn_mass", "dsa_cache_evict",
+    "EXPORTED",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -34,7 +35,7 @@ EXPORTED = (
     "dsa_indexer_kl", "dsa_indexer_kl_workspace_size", "dsa_masked_mha_fwd",
     "dsa_masked_mha_workspace_size", "dsa_debug_fault_injection", "dsa_indexer_backward",
     "dsa_forward_fused", "dsa_forward_fused_workspace_size", "dsa_paged_mla_decode",
-    "dsa_paged_mla_decode_workspace_size", "dsa_paged_attn_mass",
+    "dsa_paged_mla_decode_workspace_size", "dsa_paged_attn_mass", "dsa_cache_evict",
 )
 
 STATUS = {
@@ -108,6 +109,9 @@ def load():
     lib.dsa_paged_attn_mass.argtypes = [P, P, I64, I, I64, P, I64, I, P, I, I, I, I, I, I, F, P, P,
                                         P, I64, P]
     lib.dsa_paged_attn_mass.restype = I
+    lib.dsa_cache_evict.argtypes = [P, I64, I, I64, P, I64, I, P, I, I, P, I64, I, I, I, P, I64, I,
+                                    P, P, P, I64, P]
+    lib.dsa_cache_evict.restype = I
     lib.dsa_debug_fault_injection.argtypes = [ctypes.c_uint64, I]
     lib.dsa_debug_fault_injection.restype = None
     lib.dsa_version.argtypes = []
@@ -571,6 +575,33 @@ def dsa_paged_attn_mass(q, kv_cache, block_table, seq_lens, lse, max_len_k, sm_s
             float(sm_scale), _ptr(lse), _ptr(mass_in), _ptr(mass_out), ld,
             ctypes.c_void_p(st.cuda_stream))
     _check(rc, "dsa_paged_attn_mass")
+
+
+def dsa_cache_evict(kv_cache, block_table, seq_lens, mass, max_len_k, budget, sinks, recent,
+                    new_block_table, new_lens, idx_out, new_mass=None, stream=None):
+    """Cuts each sequence of a paged cache down to `budget` entries by mass
+    [B, >= max_len_k]: the first `sinks`, the last `recent` and the heaviest
+    between are copied to the pages of new_block_table; writes new_lens [B],
+    idx_out [B, budget] (old positions, -1 padded) and new_mass
+    [B, >= budget] (optional).  See include/dsa.h."""
+    import torch
+    _need(new_lens, torch.int32, "new_lens", 1)
+    _need(idx_out, torch.int32, "idx_out", 2)
+    cache = _paged(kv_cache, block_table, seq_lens, new_block_table=new_block_table, mass=mass,
+                   new_lens=new_lens, idx_out=idx_out, new_mass=new_mass)
+    B = seq_lens.shape[0]
+    _shape(new_lens, (B,), "new_lens")
+    _shape(idx_out, (B, int(budget)), "idx_out")
+    ld = _rows_f32(mass, B, int(max_len_k), "mass")
+    ld_new = 0 if new_mass is None else _rows_f32(new_mass, B, int(budget), "new_mass")
+    st = _stream_on(stream, kv_cache.device)
+    with torch.cuda.device(kv_cache.device):
+        rc = load().dsa_cache_evict(
+            *cache, int(max_len_k), _ptr(mass), ld, int(budget), int(sinks), int(recent),
+            _ptr(new_block_table), _table_ld(new_block_table), int(new_block_table.shape[1]),
+            _ptr(new_lens), _ptr(idx_out), _ptr(new_mass), ld_new,
+            ctypes.c_void_p(st.cuda_stream))
+    _check(rc, "dsa_cache_evict")
 
 
 def dsa_get_device_error(stream=None) -> int:

@@ -818,6 +818,49 @@ dsa_status_t dsa_paged_attn_mass(const void* q, const void* kv_cache, int64_t n_
       dsa::launch_paged_mass(tq, launches, tx, a, err, static_cast<cudaStream_t>(stream)));
 }
 
+dsa_status_t dsa_cache_evict(void* kv_cache, int64_t n_pages, int page_size, int64_t page_stride,
+                             const int32_t* block_table, int64_t block_table_ld, int max_pages,
+                             const int32_t* seq_lens, int B, int max_len_k, const float* mass,
+                             int64_t ld_mass, int budget, int sinks, int recent,
+                             const int32_t* new_block_table, int64_t new_block_table_ld,
+                             int new_max_pages, int32_t* new_lens, int32_t* idx_out,
+                             float* new_mass, int64_t ld_new_mass, void* stream) {
+  if (!mass || !new_block_table || !new_lens || !idx_out || budget < 1 || sinks < 0 || recent < 0)
+    return DSA_ERR_INVALID_ARG;
+  dsa_status_t st = check_cache(kv_cache, n_pages, page_size, page_stride, block_table,
+                                block_table_ld, max_pages, seq_lens, B, max_len_k);
+  if (st != DSA_OK) return st;
+  if (max_len_k > 262144) return DSA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(sinks) + recent > budget) return DSA_ERR_INVALID_ARG;
+  if (ld_mass < max_len_k || (new_mass && ld_new_mass < budget)) return DSA_ERR_INVALID_ARG;
+  if (new_lens == seq_lens || new_mass == mass) return DSA_ERR_INVALID_ARG;
+  const int64_t most = budget < max_len_k ? budget : max_len_k;
+  if (new_max_pages < 1 || new_block_table_ld < new_max_pages ||
+      static_cast<int64_t>(new_max_pages) * page_size < most)
+    return DSA_ERR_INVALID_ARG;
+  if (budget > (1 << 24) || static_cast<int64_t>(B) * 8 >= (int64_t(1) << 31))
+    return DSA_ERR_UNSUPPORTED;
+  if (B == 0) return DSA_OK;
+  DeviceInfo* dev = nullptr;
+  if ((st = device_info(&dev)) != DSA_OK) return st;
+  dsa::CacheEvictArgs a;
+  a.cache = cache_of(kv_cache, n_pages, page_size, page_stride, block_table, block_table_ld,
+                     max_pages, seq_lens, B, max_len_k, 0, 0);
+  a.mass = mass;
+  a.ld_mass = ld_mass;
+  a.budget = budget;
+  a.sinks = sinks;
+  a.recent = recent;
+  a.new_table = new_block_table;
+  a.new_ld = new_block_table_ld;
+  a.new_lens = new_lens;
+  a.idx = idx_out;
+  a.new_mass = new_mass;
+  a.ld_new = ld_new_mass;
+  a.num_sms = dev->num_sms;
+  return from_cuda(dsa::launch_cache_evict(a, next_err(dev), static_cast<cudaStream_t>(stream)));
+}
+
 void dsa_debug_fault_injection(uint64_t wait_limit_ns, int drop_first_key_load) {
   g_wait_limit_ns.store(wait_limit_ns);
   g_inject_indexer.store(drop_first_key_load ? dsa::kInjectDropFirstKeyLoad : 0u);

@@ -1,0 +1,324 @@
+// cache_evict.cu -- cuts the sequences of a paged latent cache down to a
+// budget of entries by a running total per entry, on sm_100a.
+//
+// A sequence of at most `budget` entries keeps them all.  A longer one keeps
+// its first `sinks`, its last `recent`, and the budget - sinks - recent
+// entries between them with the largest totals (ties to the lower position).
+// The kept entries' latents move, in their order, to the pages of a new block
+// table; their positions, totals and the new lengths are written out.
+//
+// Two launches:
+//  * select_kernel: one CTA of 1024 threads per sequence, or a cluster of eight
+//    for long ones, each CTA with its stretch of the row as order-preserving
+//    32-bit keys in shared memory, read once.  Three histogram passes (11, 11
+//    and 10 bits from the top; the CTAs read one another's histograms through
+//    distributed shared memory) find the key T of the last entry kept and how
+//    many entries equal to it are kept.  Warps own contiguous stretches, so
+//    ballots and prefixes over warps and CTAs give every kept entry its slot in
+//    position order, ties to the lower position included.  A chain of
+//    barriers and shared-memory atomics bounds it, not the row's bytes: 13 us
+//    for rows of 131072, of which reading them at the memory's rate is 0.1 us.
+//  * move_kernel: a warp moves four latents at a time, nine 16-byte loads in
+//    flight per lane; bound by the memory (2304 bytes per kept entry).
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "internal.h"
+#include "paged.cuh"
+#include "ptx.cuh"
+
+namespace dsa {
+namespace {
+
+namespace cg = cooperative_groups;
+using namespace paged;
+
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kClusterC = 8;
+constexpr int kOneCta = 8192;            // rows of at most this many entries take one CTA
+
+struct Params {
+  Cache c;
+  const float* mass;
+  int64_t ld_mass;
+  int budget, sinks, recent;
+  int wseg;               // entries per warp, a multiple of 32
+  int32_t* idx;           // [B, budget]
+  int32_t* new_lens;      // [B]
+  float* new_mass;        // [B, ld_new], nullable
+  int64_t ld_new;
+  const int32_t* new_table;
+  int64_t new_ld;
+  DevErr err;
+};
+
+// Larger totals map to larger keys; -0 equals +0, every NaN is above all numbers.
+__device__ __forceinline__ uint32_t order_key(float x) {
+  const uint32_t u = __float_as_uint(x);
+  if (x != x) return 0xFFFFFFFFu;
+  if ((u << 1) == 0) return 0x80000000u;
+  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+template <int C>
+__global__ void __launch_bounds__(kThreads, 1) select_kernel(const Params P) {
+  extern __shared__ uint32_t keys[];     // [kWarps * wseg]
+  __shared__ uint32_t hist[2][kBins];
+  __shared__ uint32_t wsum[kWarps], weq[kWarps];
+  __shared__ uint32_t found[2];          // the pass's bin, the rank left inside it
+  __shared__ uint32_t xch[2];            // this CTA's entries above T, equal to T
+  const int rank = C == 1 ? 0 : static_cast<int>(cg::this_cluster().block_rank());
+  const int b = blockIdx.x / C;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int n = seq_len(P.c, b);
+  const float* row = P.mass + static_cast<int64_t>(b) * P.ld_mass;
+  int32_t* idx = P.idx + static_cast<int64_t>(b) * P.budget;
+  float* nm = P.new_mass ? P.new_mass + static_cast<int64_t>(b) * P.ld_new : nullptr;
+  const int kept = min(n, P.budget);
+  auto sync_all = [&]() {
+    if (C == 1) __syncthreads(); else cg::this_cluster().sync();
+  };
+  if (rank == 0 && tid == 0) {
+    P.new_lens[b] = kept;
+    const int raw = __ldg(P.c.lens + b);
+    if (raw < 0 || raw > P.c.cap) raise_error(P.err, kErrBounds);
+  }
+  const bool cut = n > P.budget;
+  // what is kept whatever the totals say, and the padding behind it
+  const int head = cut ? P.sinks : kept;
+  const int tail = cut ? P.budget - P.recent : kept;
+  for (int j = rank * kThreads + tid; j < P.budget; j += C * kThreads) {
+    if (j >= head && j < tail) continue;
+    const int s = j < head ? j : (cut ? n - P.budget + j : -1);
+    idx[j] = s;
+    if (nm) nm[j] = s >= 0 ? __ldg(row + s) : 0.f;
+  }
+  const int room = P.budget - P.sinks - P.recent;
+  if (!cut || room <= 0) return;         // the whole cluster alike
+
+  // this warp's stretch of the entries in between
+  const int lo = P.sinks, m = n - P.sinks - P.recent;
+  const int w0 = (rank * kWarps + warp) * P.wseg;
+  const int len = min(max(m - w0, 0), P.wseg);
+  uint32_t* mine = keys + warp * P.wseg;
+  const float* src = row + lo + w0;
+  for (int i = lane; i < len; i += 32 * 8) {
+    float x[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) x[u] = i + 32 * u < len ? __ldg(src + i + 32 * u) : 0.f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (i + 32 * u < len) mine[i + 32 * u] = order_key(x[u]);
+  }
+  for (int i = tid; i < 2 * kBins; i += kThreads) (&hist[0][0])[i] = 0;
+  __syncthreads();
+
+  uint32_t want = static_cast<uint32_t>(room), prefix = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const int up = pass == 0 ? 32 : pass == 1 ? 21 : 10;      // bits above the digit's
+    const uint32_t mask = pass == 2 ? 1023u : 2047u;
+    uint32_t* h = hist[pass & 1];
+    for (int i = lane; i - lane < len; i += 32) {
+      const uint32_t k = i < len ? mine[i] : 0u;
+      const bool in = i < len && (pass == 0 || (k >> up) == prefix);
+      const uint32_t on = __ballot_sync(0xffffffffu, in);
+      if (on == 0) continue;
+      const uint32_t d = (k >> shift) & mask;
+      // lanes that agree (stretches of equal totals) count once
+      const int lead = __ffs(on) - 1;
+      const uint32_t first = __shfl_sync(0xffffffffu, d, lead);
+      if (__all_sync(0xffffffffu, !in || d == first)) {
+        if (lane == lead) atomicAdd(h + d, static_cast<uint32_t>(__popc(on)));
+      } else if (in) {
+        atomicAdd(h + d, 1u);
+      }
+    }
+    sync_all();
+    // the bin of the want-th largest: thread t sums bins 2047 - 2t and 2046 - 2t
+    // over the cluster, then a block scan from the top
+    uint32_t c0 = 0, c1 = 0;
+    for (int q = 0; q < C; ++q) {
+      const uint32_t* o = C == 1 ? h : cg::this_cluster().map_shared_rank(h, (rank + q) % C);
+      const uint2 x = *reinterpret_cast<const uint2*>(o + kBins - 2 - 2 * tid);
+      c0 += x.y;
+      c1 += x.x;
+    }
+    uint32_t inc = c0 + c1;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += v;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    uint32_t before = 0;
+    for (int w = 0; w < warp; ++w) before += wsum[w];
+    before += inc - c0 - c1;
+    if (before < want && want <= before + c0) {
+      found[0] = kBins - 1 - 2 * tid;
+      found[1] = want - before;
+    } else if (before + c0 < want && want <= before + c0 + c1) {
+      found[0] = kBins - 2 - 2 * tid;
+      found[1] = want - before - c0;
+    }
+    __syncthreads();
+    prefix = (prefix << (pass == 2 ? 10 : 11)) | found[0];
+    want = found[1];
+    // the next pass counts in the other buffer; no CTA reads this one's copy of
+    // it any more (all have passed this pass's barrier)
+    for (int i = tid; i < kBins; i += kThreads) hist[(pass & 1) ^ 1][i] = 0;
+    __syncthreads();
+  }
+  const uint32_t T = prefix;             // keep every key above T and the first `want` equal ones
+
+  uint32_t gt = 0, eq = 0;
+  for (int i = 0; i < len; i += 32) {
+    const uint32_t k = i + lane < len ? mine[i + lane] : 0u;
+    const bool ok = i + lane < len;
+    gt += __popc(__ballot_sync(0xffffffffu, ok && k > T));
+    eq += __popc(__ballot_sync(0xffffffffu, ok && k == T));
+  }
+  if (lane == 0) {
+    wsum[warp] = gt;
+    weq[warp] = eq;
+  }
+  __syncthreads();
+  uint32_t bg = 0, be = 0, tg = 0, te = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) {
+      bg += wsum[w];
+      be += weq[w];
+    }
+    tg += wsum[w];
+    te += weq[w];
+  }
+  if (tid == 0) {
+    xch[0] = tg;
+    xch[1] = te;
+  }
+  sync_all();
+  for (int q = 0; q < rank; ++q) {
+    const uint32_t* o = cg::this_cluster().map_shared_rank(xch, q);
+    bg += o[0];
+    be += o[1];
+  }
+  const uint32_t lt = (1u << lane) - 1;
+  for (int i = 0; i < len; i += 32) {
+    const bool ok = i + lane < len;
+    const uint32_t k = ok ? mine[i + lane] : 0u;
+    const uint32_t mg = __ballot_sync(0xffffffffu, ok && k > T);
+    const uint32_t me = __ballot_sync(0xffffffffu, ok && k == T);
+    const uint32_t g = bg + __popc(mg & lt), e = be + __popc(me & lt);
+    if (ok && (k > T || (k == T && e < want))) {
+      const int s = lo + w0 + i + lane;
+      const int64_t j = P.sinks + static_cast<int64_t>(g) + min(e, want);
+      idx[j] = s;
+      if (nm) nm[j] = __ldg(row + s);
+    }
+    bg += __popc(mg);
+    be += __popc(me);
+  }
+  // nobody's shared memory goes away while another CTA may still read it
+  if (C > 1) cg::this_cluster().sync();
+}
+
+// Four kept latents per warp: 288 pieces of 16 bytes, nine per lane.
+constexpr int kMoveRows = 4;
+__global__ void __launch_bounds__(256) move_kernel(const Params P, uint8_t* pool, int groups) {
+  const int lane = threadIdx.x % 32;
+  const int64_t all = static_cast<int64_t>(groups) * P.c.B;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * 8;
+  for (int64_t t = blockIdx.x * 8ll + threadIdx.x / 32; t < all; t += stride) {
+    const int b = static_cast<int>(t / groups);
+    const int j = static_cast<int>(t % groups) * kMoveRows + lane;
+    // lanes 0..3: where row j comes from and goes to (-1: nothing to move)
+    int64_t from = -1, to = -1;
+    if (lane < kMoveRows && j < P.budget) {
+      const int s = P.idx[static_cast<int64_t>(b) * P.budget + j];
+      if (s >= 0) {
+        const int ps = page_of(P.c, s), pd = page_of(P.c, j);
+        const int a = __ldg(P.c.table + static_cast<int64_t>(b) * P.c.table_ld + ps);
+        const int d = __ldg(P.new_table + static_cast<int64_t>(b) * P.new_ld + pd);
+        if (a < 0 || a >= P.c.n_pages || d < 0 || d >= P.c.n_pages) {
+          raise_error(P.err, kErrBounds);
+        } else {
+          from = (a * P.c.page_stride + static_cast<int64_t>(s - ps * P.c.page) * 576) * 2;
+          to = (d * P.c.page_stride + static_cast<int64_t>(j - pd * P.c.page) * 576) * 2;
+        }
+      }
+    }
+    uint4 v[9];
+#pragma unroll
+    for (int u = 0; u < 9; ++u) {
+      const int p = lane + 32 * u, r = p / 72;
+      const int64_t f = __shfl_sync(0xffffffffu, from, r);
+      if (f >= 0) v[u] = *reinterpret_cast<const uint4*>(pool + f + (p - r * 72) * 16);
+    }
+#pragma unroll
+    for (int u = 0; u < 9; ++u) {
+      const int p = lane + 32 * u, r = p / 72;
+      const int64_t d = __shfl_sync(0xffffffffu, to, r);
+      if (d >= 0) *reinterpret_cast<uint4*>(pool + d + (p - r * 72) * 16) = v[u];
+    }
+  }
+}
+
+template <int C>
+cudaError_t launch_select(const Params& P, size_t smem, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(select_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(P.c.B) * C);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, select_kernel<C>, P);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_evict(const CacheEvictArgs& a, DevErr err, cudaStream_t s) {
+  Params P;
+  P.c = a.cache;
+  P.mass = a.mass;
+  P.ld_mass = a.ld_mass;
+  P.budget = a.budget;
+  P.sinks = a.sinks;
+  P.recent = a.recent;
+  P.idx = a.idx;
+  P.new_lens = a.new_lens;
+  P.new_mass = a.new_mass;
+  P.ld_new = a.ld_new;
+  P.new_table = a.new_table;
+  P.new_ld = a.new_ld;
+  P.err = err;
+  const int C = P.c.cap <= kOneCta ? 1 : kClusterC;
+  const int warps = C * kWarps;
+  P.wseg = ((P.c.cap + warps - 1) / warps + 31) / 32 * 32;
+  const size_t smem = static_cast<size_t>(kWarps) * P.wseg * 4;
+  cudaError_t e = C == 1 ? launch_select<1>(P, smem, s) : launch_select<kClusterC>(P, smem, s);
+  if (e != cudaSuccess) return e;
+  const int most_kept = a.budget < P.c.cap ? a.budget : P.c.cap;
+  const int groups = (most_kept + kMoveRows - 1) / kMoveRows;
+  if (groups == 0) return cudaSuccess;
+  const int64_t ctas = (static_cast<int64_t>(groups) * P.c.B + 7) / 8;
+  const int64_t most = static_cast<int64_t>(a.num_sms) * 16;
+  move_kernel<<<static_cast<unsigned>(ctas < most ? ctas : most), 256, 0, s>>>(
+      P, const_cast<uint8_t*>(P.c.pool), groups);
+  return cudaGetLastError();
+}
+
+}  // namespace dsa

@@ -209,4 +209,19 @@ struct PagedMassArgs {
 cudaError_t launch_paged_mass(const CUtensorMap* tq, int launches, const CUtensorMap& tx,
                               const PagedMassArgs& a, const DevErr* err, cudaStream_t s);
 
+struct CacheEvictArgs {
+  paged::Cache cache;
+  const float* mass;
+  int64_t ld_mass;
+  int budget, sinks, recent;
+  const int32_t* new_table;
+  int64_t new_ld;
+  int32_t* new_lens;
+  int32_t* idx;
+  float* new_mass;   // nullable
+  int64_t ld_new;
+  int num_sms;
+};
+cudaError_t launch_cache_evict(const CacheEvictArgs& a, DevErr err, cudaStream_t s);
+
 }  // namespace dsa

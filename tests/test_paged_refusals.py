@@ -88,3 +88,25 @@ def mass(**kw):
 ])
 def test_mass_refuses(kw, status):
     assert mass(**kw) == status
+
+
+def evict(**kw):
+    a = dict(CACHE, mass=P, ld_m=640, budget=128, sinks=4, recent=16, nt=off(16), nt_ld=2, nt_pages=2,
+             nl=off(32), idx=P, nm=off(48), ld_nm=128)
+    a.update(kw)
+    return dsa.load().dsa_cache_evict(*cache_args(a), a["mass"], a["ld_m"], a["budget"],
+                                      a["sinks"], a["recent"], a["nt"], a["nt_ld"], a["nt_pages"],
+                                      a["nl"], a["idx"], a["nm"], a["ld_nm"], None)
+
+
+@pytest.mark.parametrize("kw,status", BAD_CACHE + [
+    (dict(mass=None), INVALID), (dict(nt=None), INVALID), (dict(nl=None), INVALID),
+    (dict(idx=None), INVALID), (dict(budget=0), INVALID), (dict(sinks=-1), INVALID),
+    (dict(recent=-1), INVALID), (dict(sinks=120, recent=9), INVALID), (dict(ld_m=639), INVALID),
+    (dict(ld_nm=127), INVALID), (dict(nt_pages=1, nt_ld=1), INVALID), (dict(nt_ld=1), INVALID),
+    (dict(nl=P), INVALID),                     # the lengths themselves
+    (dict(nm=P), INVALID),                     # the totals themselves
+    (dict(max_len=262145, ld_m=262145), UNSUPPORTED), (dict(B=0), OK),
+])
+def test_evict_refuses(kw, status):
+    assert evict(**kw) == status
