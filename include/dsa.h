@@ -387,6 +387,39 @@ DSA_API dsa_status_t dsa_masked_mha_fwd(const void* q, const void* k, const void
 DSA_API size_t dsa_masked_mha_workspace_size(int64_t total_q, int max_len_k);
 
 /*
+ * The MHA form over a sliding window and a few first tokens that stay visible
+ * (the prompt's side of a layer whose cache dsa_paged_mla_decode reads with
+ * the same window and sinks; per-head keys and values as for
+ * dsa_masked_mha_fwd):
+ *
+ *   out[q_row, h, :] = sum_s softmax_s(sm_scale * q[q_row,h,:] . k[k_row(s),h,:]) * v[k_row(s),h,:]
+ *   lse[q_row, h]    = log sum_s exp(sm_scale * q[q_row,h,:] . k[k_row(s),h,:])
+ *
+ * over the keys s <= p with s > p - window or s < sinks; window = 0 is no
+ * limit (causal attention).  Only the 128-key tiles that hold such a key are
+ * read, so the cost grows with the window, not with the sequence.
+ *
+ *  q        (device) bf16 [total_q, H, 192]: 128 dims + 64 RoPE dims per head
+ *  k        (device) bf16 [total_k, H, 192]
+ *  v        (device) bf16 [total_k, H, 128]
+ *  out      (device) bf16 [total_q, H, 128]
+ *  lse      (device, nullable) f32 [total_q, H] (natural log)
+ *  A key outside a row's window that shares a 128-key tile with one inside has
+ *  weight 0 there, so its value must be finite (0 * inf is not 0).
+ *  Supported: d_qk = 192, d_v = 128, 1 <= H <= 65535, max_len_k <= 2^24.
+ *  A sequence with more queries than keys sets DSA_ERR_BOUNDS and gets no
+ *  output.
+ *  Arithmetic: bf16 tensor-core products, fp32 accumulation and softmax (the
+ *  weights are rounded to bf16 for the product with the values).
+ */
+DSA_API dsa_status_t dsa_window_mha_fwd(const void* q, const void* k, const void* v,
+                                        const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                                        int B, int max_len_q, int max_len_k, int64_t total_q,
+                                        int64_t total_k, int H, int d_qk, int d_v, int window,
+                                        int sinks, float sm_scale, void* out, float* lse,
+                                        void* stream);
+
+/*
  * ---------------------------------------------------------------------------
  * Serving from a paged latent cache.  The pages describe the latent cache
  * ("DeepSeek-V3.2" atlas entry, "Inference efficiency": MLA keeps one latent

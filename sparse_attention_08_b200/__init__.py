@@ -20,7 +20,7 @@ __all__ = [
     "dsa_debug_fault_injection", "dsa_indexer_backward", "dsa_forward_fused",
     "dsa_forward_fused_workspace_size", "dsa_paged_mla_decode",
     "dsa_paged_mla_decode_workspace_size", "dsa_paged_attn_mass", "dsa_cache_evict",
-    "EXPORTED",
+    "dsa_window_mha_fwd", "EXPORTED",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -36,6 +36,7 @@ EXPORTED = (
     "dsa_masked_mha_workspace_size", "dsa_debug_fault_injection", "dsa_indexer_backward",
     "dsa_forward_fused", "dsa_forward_fused_workspace_size", "dsa_paged_mla_decode",
     "dsa_paged_mla_decode_workspace_size", "dsa_paged_attn_mass", "dsa_cache_evict",
+    "dsa_window_mha_fwd",
 )
 
 STATUS = {
@@ -112,6 +113,8 @@ def load():
     lib.dsa_cache_evict.argtypes = [P, I64, I, I64, P, I64, I, P, I, I, P, I64, I, I, I, P, I64, I,
                                     P, P, P, I64, P]
     lib.dsa_cache_evict.restype = I
+    lib.dsa_window_mha_fwd.argtypes = [P, P, P, P, P, I, I, I, I64, I64, I, I, I, I, I, F, P, P, P]
+    lib.dsa_window_mha_fwd.restype = I
     lib.dsa_debug_fault_injection.argtypes = [ctypes.c_uint64, I]
     lib.dsa_debug_fault_injection.restype = None
     lib.dsa_version.argtypes = []
@@ -454,6 +457,42 @@ def dsa_masked_mha_fwd(q, k, v, idx, cu_seqlens_q, cu_seqlens_k, B, max_len_q, m
                                    int(topk), float(sm_scale), _ptr(out), _ptr(lse),
                                    _ptr(workspace), int(workspace.numel()), _stream(stream))
     _check(rc, "dsa_masked_mha_fwd")
+
+
+def dsa_window_mha_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, B, max_len_q, max_len_k, window,
+                       sinks, sm_scale, out, lse=None, stream=None):
+    """Per-head attention of q [T_q, H, 192] over k [T_k, H, 192], v
+    [T_k, H, 128], each query over its last `window` keys (0: all) and the
+    sequence's first `sinks` (see include/dsa.h); writes out [T_q, H, 128]
+    (bf16) and lse [T_q, H] (fp32, optional)."""
+    import torch
+    _need(q, torch.bfloat16, "q", 3)
+    _need(k, torch.bfloat16, "k", 3)
+    _need(v, torch.bfloat16, "v", 3)
+    _need(cu_seqlens_q, torch.int32, "cu_seqlens_q", 1)
+    _need(cu_seqlens_k, torch.int32, "cu_seqlens_k", 1)
+    _need(out, torch.bfloat16, "out", 3)
+    _need(lse, torch.float32, "lse", 2)
+    T_q, H, d_qk = q.shape
+    T_k, d_v = k.shape[0], v.shape[2]
+    _shape(k, (T_k, H, d_qk), "k")
+    _shape(v, (T_k, H, d_v), "v")
+    _shape(out, (T_q, H, d_v), "out")
+    _shape(lse, (T_q, H), "lse")
+    _shape(cu_seqlens_q, (int(B) + 1,), "cu_seqlens_q")
+    _shape(cu_seqlens_k, (int(B) + 1,), "cu_seqlens_k")
+    for t, name in ((k, "k"), (v, "v"), (cu_seqlens_q, "cu_seqlens_q"),
+                    (cu_seqlens_k, "cu_seqlens_k"), (out, "out"), (lse, "lse")):
+        if t is not None and t.device != q.device:
+            raise ValueError(f"{name} must be on q's device, {q.device}")
+    st = _stream_on(stream, q.device)
+    with torch.cuda.device(q.device):
+        rc = load().dsa_window_mha_fwd(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), int(B),
+            int(max_len_q), int(max_len_k), int(T_q), int(T_k), int(H), int(d_qk), int(d_v),
+            int(window), int(sinks), float(sm_scale), _ptr(out), _ptr(lse),
+            ctypes.c_void_p(st.cuda_stream))
+    _check(rc, "dsa_window_mha_fwd")
 
 
 def _stream_on(stream, device):

@@ -338,6 +338,46 @@ dsa_status_t dsa_masked_mha_fwd(const void* q, const void* k, const void* v, con
                                           static_cast<cudaStream_t>(stream)));
 }
 
+dsa_status_t dsa_window_mha_fwd(const void* q, const void* k, const void* v,
+                                const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int B,
+                                int max_len_q, int max_len_k, int64_t total_q, int64_t total_k,
+                                int H, int d_qk, int d_v, int window, int sinks, float sm_scale,
+                                void* out, float* lse, void* stream) {
+  dsa_status_t st = check_varlen(cu_seqlens_q, cu_seqlens_k, B, max_len_q, max_len_k, total_q,
+                                 total_k);
+  if (st != DSA_OK) return st;
+  if (!q || !k || !v || !out || window < 0 || sinks < 0) return DSA_ERR_INVALID_ARG;
+  if (d_qk != 192 || d_v != 128 || H < 1 || H > 65535 || max_len_k > (1 << 24))
+    return DSA_ERR_UNSUPPORTED;
+  if (!(sm_scale > 0.f) || sm_scale != sm_scale) return DSA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out)) return DSA_ERR_ALIGNMENT;
+  if (total_q >= (int64_t(1) << 31) || total_k >= (int64_t(1) << 31)) return DSA_ERR_UNSUPPORTED;
+  if (total_q == 0 || B == 0) return DSA_OK;
+  if (total_k == 0) return DSA_ERR_INVALID_ARG;
+  DeviceInfo* dev = nullptr;
+  if ((st = device_info(&dev)) != DSA_OK) return st;
+  CUtensorMap tq, tk, tv;
+  if ((st = encode_3d_bf16(&tq, q, 192, H, total_q, 64, 128)) != DSA_OK) return st;
+  if ((st = encode_3d_bf16(&tk, k, 192, H, total_k, 64, 128)) != DSA_OK) return st;
+  if ((st = encode_3d_bf16(&tv, v, 128, H, total_k, 64, 128)) != DSA_OK) return st;
+  dsa::WindowMhaArgs a;
+  a.cu_q = cu_seqlens_q;
+  a.cu_k = cu_seqlens_k;
+  a.B = B;
+  a.max_len_q = max_len_q;
+  a.total_k = total_k;
+  a.H = H;
+  // positions stay below 2^24: a longer window or more first tokens reach everything
+  a.window = window < (1 << 25) ? window : (1 << 25);
+  a.sinks = sinks < (1 << 25) ? sinks : (1 << 25);
+  a.sm_scale = sm_scale;
+  a.out = out;
+  a.lse = lse;
+  a.num_sms = dev->num_sms;
+  return from_cuda(dsa::launch_window_mha(tq, tk, tv, a, next_err(dev),
+                                          static_cast<cudaStream_t>(stream)));
+}
+
 size_t dsa_indexer_kl_workspace_size(int64_t total_q, int H, int k) {
   if (total_q < 0 || !mla_heads_ok(H) || k < 1 || k > 4096) return 0;
   return dsa::indexer_kl_workspace_bytes(total_q, H, k);

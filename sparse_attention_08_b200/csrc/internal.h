@@ -222,6 +222,20 @@ struct CacheEvictArgs {
   int64_t ld_new;
   int num_sms;
 };
+struct WindowMhaArgs {
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int B, max_len_q;
+  int64_t total_k;
+  int H, window, sinks;
+  float sm_scale;
+  void* out;
+  float* lse;        // nullable
+  int num_sms;
+};
+cudaError_t launch_window_mha(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                              const WindowMhaArgs& a, DevErr err, cudaStream_t s);
+
 cudaError_t launch_cache_evict(const CacheEvictArgs& a, DevErr err, cudaStream_t s);
 
 }  // namespace dsa

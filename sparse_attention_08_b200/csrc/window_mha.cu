@@ -1,0 +1,568 @@
+// window_mha.cu -- attention of a prompt in the MHA form of MLA over a sliding
+// window and a few first tokens that stay visible, on sm_100a.
+//
+//   out[t,h,:] = sum_{s in V_t} softmax_s(scale q[t,h,:] . k[s,h,:]) v[s,h,:]
+//   lse[t,h]   = log sum_{s in V_t} exp(scale q[t,h,:] . k[s,h,:])
+//
+// with V_t = { s <= p : s > p - window or s < sinks } for the query at
+// position p (every head with its own 192-d key and 128-d value).
+//
+// A persistent grid of one CTA per SM.  A work item is a pair of 128-query
+// tiles of one sequence and head; it walks the 128-key tiles that hold a key some row
+// of the pair sees (the first tokens' tiles, then the window's).  The two
+// query tiles have their own score and output accumulators in TMEM, and the
+// MMA warp alternates between them, so the softmax of one runs under the
+// products of the other:
+//
+//   ... P V (tile 0, j)  S (tile 0, j+1)  P V (tile 1, j)  S (tile 1, j+1) ...
+//
+//  warp 0      TMA: queries, then keys and values as 16 KB boxes (128 rows x 64
+//              columns) through one ring of eight; a key tile is three boxes,
+//              a value tile two, and a box is reloaded as soon as both query
+//              tiles are done with it;
+//  warp 1      MMA issuer: S = Q K^T (12 MMAs, M128 N128 K16), O += P V (8
+//              MMAs, P read from TMEM, V MN-major from shared memory);
+//  warps 4..11 two warpgroups, one per query tile, a thread one row: P over
+//              the scores' own columns, no exchange between threads.  The
+//              running maximum of the tile before serves as the exponentials'
+//              reference; only where a score exceeds it by more than 2^8 is the
+//              tile's maximum taken first and O rescaled.
+// TMEM: S (and P) at columns 0 and 128, O at 256 and 384.
+//
+// Bound by the tensor cores: 20 MMAs of 64 cycles per tile pair of 128 x 128,
+// of which the softmax's exponentials (128 x 128 at 16 a cycle) take four fifths.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "internal.h"
+#include "paged.cuh"
+#include "ptx.cuh"
+
+namespace dsa {
+namespace {
+
+using paged::all_wait;
+using paged::max3;
+using paged::tma_load_3d;
+
+constexpr int kBM = 128;
+constexpr int kBN = 128;
+constexpr int kDv = 128;
+constexpr uint32_t kBox = 128 * 128;                   // 128 rows of 64 columns: 16 KB
+constexpr int kRing = 8;
+constexpr uint32_t kOffQ = 0;                          // two tiles of three boxes
+constexpr uint32_t kOffRing = 6 * kBox;
+constexpr uint32_t kOffBar = kOffRing + kRing * kBox;
+// barriers: full[4] (units), empty[8] (boxes), q_full[2], q_empty[2], s_full[2], p_full[2],
+// o_full[2], drain
+constexpr uint32_t kNumBars = 4 + kRing + 10 + 1;
+constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;
+constexpr uint32_t kSmem = kOffMisc + 16 + 1024;
+constexpr int kThreads = 384;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 256;
+constexpr uint32_t kIdescS = instr_desc(kFmtBF16, kFmtBF16, 0, 0, kBM, kBN);
+constexpr uint32_t kIdescPV = instr_desc(kFmtBF16, kFmtBF16, 0, 1, kBM, kDv);
+constexpr uint32_t kIdescPV64 = instr_desc(kFmtBF16, kFmtBF16, 0, 1, kBM, 64);
+constexpr float kSlack = 8.0f;                         // log2 units above the reference
+
+static_assert(kSmem <= 232448, "shared memory budget");
+
+struct Params {
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int64_t total_k;
+  int B, H;
+  int pairs;                // query-tile pairs per sequence slot
+  int window, sinks;        // window 0: no limit
+  int64_t items;
+  float scale_log2;
+  __nv_bfloat16* out;
+  float* lse;
+  DevErr err;
+};
+
+// One work item: query rows [q0, q0 + rows) of sequence b, head h.
+struct Item {
+  int b, h, q0, rows, tiles;   // tiles: query tiles, 1 or 2 (0: nothing here)
+  int cq, ck, len_k, off;      // query i of the sequence sits at position off + i
+  int a, w0, n;                // key tiles: the first a, then from w0 on; n in all
+  __device__ __forceinline__ int key_tile(int i) const { return i < a ? i : w0 + (i - a); }
+};
+
+__device__ __forceinline__ Item item_of(const Params& P, int64_t i) {
+  Item x;
+  // the query tiles of a head are neighbours: they share its keys in L2; the
+  // last ones, which may have the most keys, go first
+  const int64_t bh = i / P.pairs;
+  x.b = static_cast<int>(bh / P.H);
+  x.h = static_cast<int>(bh - static_cast<int64_t>(x.b) * P.H);
+  x.q0 = (P.pairs - 1 - static_cast<int>(i - bh * P.pairs)) * (2 * kBM);
+  x.cq = __ldg(P.cu_q + x.b);
+  x.ck = __ldg(P.cu_k + x.b);
+  const int len_q = __ldg(P.cu_q + x.b + 1) - x.cq;
+  x.len_k = __ldg(P.cu_k + x.b + 1) - x.ck;
+  x.off = x.len_k - len_q;
+  x.rows = min(2 * kBM, len_q - x.q0);
+  x.tiles = x.rows <= 0 || x.off < 0 ? 0 : (x.rows > kBM ? 2 : 1);
+  const int p0 = x.off + x.q0, p1 = p0 + x.rows - 1;
+  const int lo = P.window > 0 ? max(0, p0 - P.window + 1) : 0;
+  x.a = (min(P.sinks, lo) + kBN - 1) / kBN;
+  x.w0 = max(lo / kBN, x.a);
+  x.n = x.a + p1 / kBN + 1 - x.w0;
+  return x;
+}
+
+// What query tile t (rows of one accumulator) sees of key tile j.
+struct Rows {
+  int p0, p1, lo;              // positions of its rows, first key of its first row's window
+  __device__ __forceinline__ Rows(const Params& P, const Item& x, int t) {
+    p0 = x.off + x.q0 + t * kBM;
+    p1 = x.off + x.q0 + min(x.rows, (t + 1) * kBM) - 1;
+    lo = P.window > 0 ? max(0, p0 - P.window + 1) : 0;
+  }
+  __device__ __forceinline__ bool any(const Params& P, int j) const {
+    return j * kBN <= p1 && (j * kBN + kBN > lo || j * kBN < P.sinks);
+  }
+  __device__ __forceinline__ bool all(const Params& P, int j) const {
+    return j * kBN + kBN - 1 <= p0 &&
+           (P.window == 0 || j * kBN > p1 - P.window || j * kBN + kBN <= P.sinks);
+  }
+};
+
+// Bits [lo, hi) of a 32-bit word.
+__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
+  lo = min(max(lo, 0), 32);
+  hi = min(max(hi, 0), 32);
+  const uint32_t below = hi == 32 ? 0xFFFFFFFFu : (1u << hi) - 1u;
+  const uint32_t skip = lo == 32 ? 0xFFFFFFFFu : (1u << lo) - 1u;
+  return below & ~skip;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    window_mha_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                      const __grid_constant__ CUtensorMap tv, const Params P) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + kOffBar;
+  auto full = [&](uint32_t unit) { return bar0 + 8u * (unit & 3); };
+  auto empty = [&](uint32_t box) { return bar0 + 8u * (4 + (box & (kRing - 1))); };
+  auto q_full = [&](int t) { return bar0 + 8u * (4 + kRing + t); };
+  auto q_empty = [&](int t) { return bar0 + 8u * (6 + kRing + t); };
+  auto s_full = [&](int t) { return bar0 + 8u * (8 + kRing + t); };
+  auto p_full = [&](int t) { return bar0 + 8u * (10 + kRing + t); };
+  auto o_full = [&](int t) { return bar0 + 8u * (12 + kRing + t); };
+  const uint32_t drain = bar0 + 8u * (14 + kRing);
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + kOffMisc);
+
+  const int warp = threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 4; ++i) mbar_init(full(i), 1);
+    for (int i = 0; i < kRing; ++i) mbar_init(empty(i), 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(q_full(t), 1);
+      mbar_init(q_empty(t), 1);
+      mbar_init(s_full(t), 1);
+      mbar_init(p_full(t), 4);
+      mbar_init(o_full(t), 1);
+    }
+    mbar_init(drain, 1);
+    fence_barrier_init();
+    tma_prefetch_desc(&tq);
+    tma_prefetch_desc(&tk);
+    tma_prefetch_desc(&tv);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA
+    uint32_t box = 0, unit = 0, nq0 = 0, nq1 = 0;
+    bool ok = true;
+    // one unit (a key or a value tile): its boxes, announced on its barrier
+    auto load = [&](const CUtensorMap* m, int boxes, int h, int row) {
+#pragma unroll 1
+      for (int c = 0; ok && c < boxes; ++c, ++box) {
+        ok = all_wait(empty(box), ((box / kRing) & 1) ^ 1, P.err);
+        if (!ok) break;
+        if (lane == 0) {
+          if (c == 0) mbar_arrive_expect_tx(full(unit), static_cast<uint32_t>(boxes) * kBox);
+          tma_load_3d(sbase + kOffRing + (box & (kRing - 1)) * kBox, m, 64 * c, h, row, full(unit));
+        }
+        __syncwarp();
+      }
+      if (ok) ++unit;
+    };
+#pragma unroll 1
+    for (int64_t i = blockIdx.x; ok && i < P.items; i += gridDim.x) {
+      const Item x = item_of(P, i);
+      // (more queries than keys: there is no such sequence)
+      if (x.off < 0 && x.rows > 0 && lane == 0) raise_error(P.err, kErrBounds);
+      if (x.tiles == 0) continue;
+#pragma unroll 1
+      for (int t = 0; ok && t < x.tiles; ++t) {
+        ok = all_wait(q_empty(t), ((t ? nq1 : nq0) & 1) ^ 1, P.err);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(q_full(t), 3 * kBox);
+#pragma unroll 1
+          for (int c = 0; c < 3; ++c)
+            tma_load_3d(sbase + kOffQ + (3 * t + c) * kBox, &tq, 64 * c, x.h, x.cq + x.q0 + t * kBM,
+                        q_full(t));
+        }
+        __syncwarp();
+        if (t) ++nq1; else ++nq0;
+      }
+#pragma unroll 1
+      for (int j = 0; ok && j < x.n; ++j) {
+        const int row = x.ck + x.key_tile(j) * kBN;
+        load(&tk, 3, x.h, row);
+        load(&tv, 2, x.h, row);
+      }
+    }
+    // after a failure, let the copies in flight land before the memory goes
+    if (!ok && lane == 0) {
+      if (nq0 > 0) mbar_wait_drain(q_full(0), (nq0 - 1) & 1, P.err);
+      if (nq1 > 0) mbar_wait_drain(q_full(1), (nq1 - 1) & 1, P.err);
+      for (uint32_t u = unit > 2 ? unit - 2 : 0; u <= unit; ++u)
+        if (u < unit || box > 0) mbar_wait_drain(full(u), (u / 4) & 1, P.err);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA
+    const uint64_t dQ0 = smem_desc(sbase + kOffQ, 16, 1024, kSwizzle128B);
+    const uint64_t dR = smem_desc(sbase + kOffRing, 16, 1024, kSwizzle128B);
+    // a value box: 64 of the 128 dims, MN-major
+    const uint64_t dV = smem_desc(sbase + kOffRing, kBox, 1024, kSwizzle128B);
+    // phases of p_full and q_full: bit t (in registers, not in an array)
+    uint32_t box = 0, unit = 0, ns = 0, nq = 0;
+    bool ok = true;
+#pragma unroll 1
+    for (int64_t it = blockIdx.x; ok && it < P.items; it += gridDim.x) {
+      const Item x = item_of(P, it);
+      if (x.tiles == 0) continue;
+      const Rows r0(P, x, 0), r1(P, x, 1);
+      auto needs = [&](int t, int i) -> bool {
+        const int j = x.key_tile(i);
+        return t == 0 ? r0.any(P, j) : x.tiles > 1 && r1.any(P, j);
+      };
+      // the query tiles' last key tiles
+      int last0 = x.n - 1, last1 = x.n - 1;
+      while (last0 > 0 && !needs(0, last0)) --last0;
+      while (x.tiles > 1 && last1 > 0 && !needs(1, last1)) --last1;
+      uint32_t begun = 0;         // bit t: O of tile t holds something
+      // S of query tile t with the key tile in the ring at box kb
+      auto scores = [&](int t, int i, uint32_t kb) {
+        if (elect_one()) {
+#pragma unroll
+          for (int c = 0; c < 3; ++c) {
+            const uint64_t a = dQ0 + (((3 * t + c) * kBox) >> 4);
+            const uint64_t b = dR + ((((kb + c) & (kRing - 1)) * kBox) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_f16(tmem + 128u * t, a + ((kk * 32) >> 4), b + ((kk * 32) >> 4), kIdescS,
+                      (c | kk) != 0 ? 1u : 0u);
+          }
+          mma_commit(s_full(t));
+          if (i == (t ? last1 : last0)) mma_commit(q_empty(t));
+        }
+        __syncwarp();
+      };
+      // O += P V of query tile t with the value tile at box vb
+      auto values = [&](int t, int i, uint32_t vb) {
+        if (elect_one()) {
+          const uint32_t more = (begun >> t) & 1;
+          const uint32_t p = tmem + 128u * t, o = tmem + kColO + 128u * t;
+          const uint64_t b0 = dV + (((vb & (kRing - 1)) * kBox) >> 4);
+          if ((vb & (kRing - 1)) != kRing - 1) {
+#pragma unroll
+            for (int kk = 0; kk < kBN / 16; ++kk)
+              mma_f16_ts(o, p + 8u * kk, b0 + ((kk * 2048) >> 4), kIdescPV, kk > 0 ? 1u : more);
+          } else {
+            // one value tile in eight wraps around the ring's end: its two
+            // 64-dim boxes are not neighbours, and take an MMA each
+#pragma unroll
+            for (int kk = 0; kk < kBN / 16; ++kk) {
+              mma_f16_ts(o, p + 8u * kk, b0 + ((kk * 2048) >> 4), kIdescPV64, kk > 0 ? 1u : more);
+              mma_f16_ts(o + 64u, p + 8u * kk, dV + ((kk * 2048) >> 4), kIdescPV64, kk > 0 ? 1u : more);
+            }
+          }
+          if (i == (t ? last1 : last0)) mma_commit(o_full(t));
+        }
+        begun |= 1u << t;
+        __syncwarp();
+      };
+      auto free_boxes = [&](uint32_t b, int n) {
+        if (elect_one())
+          for (int c = 0; c < n; ++c) mma_commit(empty(b + c));
+        __syncwarp();
+      };
+      // the first key tile
+      for (int t = 0; ok && t < x.tiles; ++t) {
+        ok = all_wait(q_full(t), (nq >> t) & 1, P.err);
+        nq ^= 1u << t;
+      }
+      ok = ok && all_wait(full(unit), (unit / 4) & 1, P.err);
+      if (!ok) break;
+      tc_fence_after();
+      if (needs(0, 0)) scores(0, 0, box);
+      if (needs(1, 0)) scores(1, 0, box);
+      free_boxes(box, 3);
+      box += 3;
+      ++unit;
+#pragma unroll 1
+      for (int i = 0; ok && i < x.n; ++i) {
+        const uint32_t vb = box, kb = box + 2;
+        const bool more = i + 1 < x.n;
+        ok = all_wait(full(unit), (unit / 4) & 1, P.err);
+        if (!ok) break;
+        // value rows past the sequence are another's (or unwritten memory):
+        // their weights are 0, and so must they be (0 * NaN is not)
+        const int rem = x.len_k - x.key_tile(i) * kBN;
+        if (rem < kBN && x.ck + x.len_k < P.total_k) {
+          for (int e = rem * 8 + lane; e < kBN * 8; e += 32) {
+            const uint32_t o = (e >> 3) * 128 + (e & 7) * 16;
+            *reinterpret_cast<uint4*>(smem + kOffRing + (vb & (kRing - 1)) * kBox + o) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(smem + kOffRing + ((vb + 1) & (kRing - 1)) * kBox + o) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        ++unit;
+        bool have_k = false;
+#pragma unroll 1
+        for (int t = 0; ok && t < x.tiles; ++t) {
+          if (needs(t, i)) {
+            ok = all_wait(p_full(t), (ns >> t) & 1, P.err);
+            if (!ok) break;
+            ns ^= 1u << t;
+            tc_fence_after();
+            values(t, i, vb);
+          }
+          if (t + 1 == x.tiles) free_boxes(vb, 2);
+          if (more) {
+            if (!have_k) {
+              ok = all_wait(full(unit), (unit / 4) & 1, P.err);
+              if (!ok) break;
+              tc_fence_after();
+              have_k = true;
+            }
+            if (needs(t, i + 1)) scores(t, i + 1, kb);
+            if (t + 1 == x.tiles) free_boxes(kb, 3);
+          }
+        }
+        box += 2;
+        if (more) {
+          box += 3;
+          ++unit;
+        }
+      }
+    }
+    mma_commit_warp(drain);
+    if (lane == 0) mbar_wait_drain(drain, 0, P.err);
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ softmax
+    const int t = (warp - 4) >> 2;
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t sc = tmem + lane_base + 128u * t;          // scores, then P
+    const uint32_t oc = tmem + lane_base + kColO + 128u * t;
+    uint32_t ns = 0, no = 0;
+    bool ok = true;
+#pragma unroll 1
+    for (int64_t it = blockIdx.x; ok && it < P.items; it += gridDim.x) {
+      const Item x = item_of(P, it);
+      if (t >= x.tiles) continue;
+      const Rows rr(P, x, t);
+      const bool row_ok = t * kBM + r < x.rows;
+      const int i = x.q0 + (row_ok ? t * kBM + r : x.rows - 1);   // local query index
+      const int p = x.off + i;
+      const int first = P.window > 0 ? max(0, p - P.window + 1) : 0;
+      float m = -INFINITY;
+      float2 l = make_float2(0.f, 0.f);
+#pragma unroll 1
+      for (int k = 0; k < x.n; ++k) {
+        const int j = x.key_tile(k);
+        if (!rr.any(P, j)) continue;
+        ok = all_wait(s_full(t), ns & 1, P.err);
+        if (!ok) break;
+        ++ns;
+        tc_fence_after();
+        uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
+        const bool whole = rr.all(P, j);
+        if (!whole) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int s0 = j * kBN + 32 * c;
+            see[c] = bit_range(first - s0, p + 1 - s0) | bit_range(0, min(P.sinks, p + 1) - s0);
+          }
+        }
+        auto load = [&](int c, uint32_t (&v)[32]) {
+          tmem_ld_32x32b_x32(sc + 32u * c, v);
+          tmem_wait_ld();
+          if (!whole) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((see[c] >> e) & 1u)) v[e] = 0xff800000u;
+          }
+        };
+        uint32_t pk[64];
+        float2 sum;
+        float top;
+        // the weights over the reference m, and the largest exponent among them
+        auto weigh = [&]() {
+          const float nm = m == -INFINITY ? 0.f : -m;
+          const float2 s2 = make_float2(P.scale_log2, P.scale_log2), n2 = make_float2(nm, nm);
+          top = -INFINITY;
+          sum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[32];
+            load(c, v);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float2 y = __ffma2_rn(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])),
+                                          s2, n2);
+              top = max3(top, y.x, y.y);
+              const float2 w = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+              sum = __fadd2_rn(sum, w);
+              pk[16 * c + e] = pack_bf16x2(w.x, w.y);
+            }
+          }
+        };
+        bool again = m == -INFINITY;
+        if (!__all_sync(0xffffffffu, again)) {
+          weigh();
+          again = again || top > kSlack;
+        }
+        if (__any_sync(0xffffffffu, again)) {
+          // the tile's maximum first
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(sc + 32u * c, v);
+            tmem_wait_ld();
+            const uint32_t bits = c == 0 ? see[0] : c == 1 ? see[1] : c == 2 ? see[2] : see[3];
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if ((bits >> e) & 1u) mx = fmaxf(mx, __uint_as_float(v[e]));
+          }
+          mx *= P.scale_log2;
+          float al = 1.f;
+          if (mx > m) {
+            al = fast_exp2(m - mx);                   // 0 when m = -inf
+            m = mx;
+            l = __fmul2_rn(l, make_float2(al, al));
+          }
+          // O is complete up to the tile before: its product was issued before
+          // these scores'
+          if (k > 0 && __any_sync(0xffffffffu, al != 1.f)) {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(oc + 32u * c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+              tmem_st_32x32b_x32(oc + 32u * c, o);
+            }
+          }
+          weigh();
+        }
+        l = __fadd2_rn(l, sum);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t w[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) w[e] = pk[32 * c + e];
+          tmem_st_32x32b_x32(sc + 32u * c, w);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(t));
+      }
+      if (!ok) break;
+      // ---------------------------------------------------------- read-out
+      ok = all_wait(o_full(t), no & 1, P.err);
+      if (!ok) break;
+      ++no;
+      tc_fence_after();
+      const float total = l.x + l.y;
+      const float inv = total == 0.f ? 0.f : 1.f / total;
+      const int64_t row = static_cast<int64_t>(x.cq + i) * P.H + x.h;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[32];
+        tmem_ld_32x32b_x32(oc + 32u * c, o);
+        tmem_wait_ld();
+        if (row_ok) {
+          uint4* dst = reinterpret_cast<uint4*>(P.out + row * kDv + 32 * c);
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint4 w;
+            w.x = pack_bf16x2(__uint_as_float(o[e + 0]) * inv, __uint_as_float(o[e + 1]) * inv);
+            w.y = pack_bf16x2(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+            w.z = pack_bf16x2(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+            w.w = pack_bf16x2(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+            dst[e / 8] = w;
+          }
+        }
+      }
+      if (row_ok && P.lse)
+        P.lse[row] = total == 0.f ? -INFINITY : (m + log2f(total)) * 0.69314718055994531f;
+      // the next item's first product over O waits for this warp's P, which
+      // comes after these reads
+      tc_fence_before();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_window_mha(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                              const WindowMhaArgs& a, DevErr err, cudaStream_t s) {
+  Params P;
+  P.cu_q = a.cu_q;
+  P.cu_k = a.cu_k;
+  P.total_k = a.total_k;
+  P.B = a.B;
+  P.H = a.H;
+  P.pairs = (a.max_len_q + 2 * kBM - 1) / (2 * kBM);
+  P.window = a.window;
+  P.sinks = a.sinks;
+  P.items = static_cast<int64_t>(a.B) * a.H * P.pairs;
+  P.scale_log2 = a.sm_scale * 1.4426950408889634f;
+  P.out = reinterpret_cast<__nv_bfloat16*>(a.out);
+  P.lse = a.lse;
+  P.err = err;
+  cudaError_t e = cudaFuncSetAttribute(window_mha_kernel,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(kSmem));
+  if (e != cudaSuccess) return e;
+  const unsigned grid = static_cast<unsigned>(P.items < a.num_sms ? P.items : a.num_sms);
+  window_mha_kernel<<<grid, kThreads, kSmem, s>>>(tq, tk, tv, P);
+  return cudaGetLastError();
+}
+
+}  // namespace dsa

@@ -110,3 +110,25 @@ def evict(**kw):
 ])
 def test_evict_refuses(kw, status):
     assert evict(**kw) == status
+
+
+def window_mha(**kw):
+    a = dict(q=P, k=P, v=P, cq=P, ck=P, B=1, mlq=64, mlk=64, tq=64, tk=64, H=128, d_qk=192, d_v=128,
+             window=32, sinks=4, scale=0.07, out=P, lse=P)
+    a.update(kw)
+    return dsa.load().dsa_window_mha_fwd(*[a[n] for n in (
+        "q", "k", "v", "cq", "ck", "B", "mlq", "mlk", "tq", "tk", "H", "d_qk", "d_v", "window",
+        "sinks", "scale", "out", "lse")], None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID),
+    (dict(out=None), INVALID), (dict(cq=None), INVALID), (dict(window=-1), INVALID),
+    (dict(sinks=-1), INVALID), (dict(scale=0.0), INVALID), (dict(mlq=65), INVALID),
+    (dict(tq=65), INVALID), (dict(tk=0), INVALID), (dict(H=0), UNSUPPORTED),
+    (dict(d_qk=128), UNSUPPORTED), (dict(d_v=192), UNSUPPORTED),
+    (dict(mlk=(1 << 24) + 1), UNSUPPORTED), (dict(q=off(4)), ALIGN), (dict(out=off(8)), ALIGN),
+    (dict(tq=0), OK), (dict(B=0, tq=0, tk=0), OK),
+])
+def test_window_mha_refuses(kw, status):
+    assert window_mha(**kw) == status
