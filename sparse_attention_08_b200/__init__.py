@@ -459,6 +459,97 @@ def dsa_masked_mha_fwd(q, k, v, idx, cu_seqlens_q, cu_seqlens_k, B, max_len_q, m
     _check(rc, "dsa_masked_mha_fwd")
 
 
+class _On:
+    """The device and stream a call runs on: the given stream (a torch stream or
+    a raw handle), or the device's current one.  Entered around the launch; on
+    the current device and stream, the common case, that does nothing."""
+
+    __slots__ = ("handle", "_ctx")
+
+    def __init__(self, device, stream):
+        import torch
+        self._ctx = ()
+        if device.index != torch.cuda.current_device():
+            self._ctx = (torch.cuda.device(device),)
+        if stream is None:
+            self.handle = torch.cuda.current_stream(device).cuda_stream
+        else:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            self.handle = stream.cuda_stream
+            # a workspace allocated inside belongs to this stream
+            self._ctx += (torch.cuda.stream(stream),)
+
+    def __enter__(self):
+        for c in self._ctx:
+            c.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        for c in reversed(self._ctx):
+            c.__exit__(*exc)
+
+
+def _ten(t, dtype, shape, device, name):
+    """Checks a contiguous tensor (None passes) and returns its address.  shape:
+    the sizes, None where any will do."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    have = t.shape
+    if len(have) != len(shape) or any(w is not None and h != w for h, w in zip(have, shape)):
+        want = tuple("any" if w is None else w for w in shape)
+        raise ValueError(f"{name} must have shape {want}, got {tuple(have)}")
+    return t.data_ptr()
+
+
+def _rows(t, dtype, B, least, device, name):
+    """Checks a matrix [B, >= least] whose rows are contiguous (None passes);
+    returns its address and row stride."""
+    if t is None:
+        return None, 0
+    if t.dtype != dtype or t.device != device or t.dim() != 2 or t.shape[0] != B:
+        raise ValueError(f"{name} must be a {dtype} matrix of {B} rows on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    n = t.shape[1]
+    if n < least:
+        raise ValueError(f"{name} must have at least {least} columns, got {n}")
+    if n > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), (t.stride(0) if B > 1 else n)
+
+
+def _cuda(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _cache(kv_cache, block_table, seq_lens):
+    """Checks the tensors of a paged cache; returns its arguments in the C ABI's
+    order, the number of sequences last, and the device."""
+    import torch
+    dev = _cuda(kv_cache, "kv_cache")
+    if kv_cache.dtype != torch.bfloat16 or kv_cache.dim() != 3 or kv_cache.shape[2] != 576:
+        raise ValueError("kv_cache must be a torch.bfloat16 tensor [n_pages, page_size, 576]")
+    n_pages, page, _ = kv_cache.shape
+    stride, row, col = kv_cache.stride()
+    if n_pages == 1:
+        stride = page * 576
+    if col != 1 or (page > 1 and row != 576):
+        raise ValueError("kv_cache rows must lie one after the other within a page")
+    B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
+    lens = _ten(seq_lens, torch.int32, (B,), dev, "seq_lens")
+    table, ld = _rows(block_table, torch.int32, B, 1, dev, "block_table")
+    return (kv_cache.data_ptr(), n_pages, page, stride, table, ld, block_table.shape[1], lens,
+            B), dev
+
+
 def dsa_window_mha_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, B, max_len_q, max_len_k, window,
                        sinks, sm_scale, out, lse=None, stream=None):
     """Per-head attention of q [T_q, H, 192] over k [T_k, H, 192], v
@@ -466,83 +557,22 @@ def dsa_window_mha_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, B, max_len_q, max_le
     sequence's first `sinks` (see include/dsa.h); writes out [T_q, H, 128]
     (bf16) and lse [T_q, H] (fp32, optional)."""
     import torch
-    _need(q, torch.bfloat16, "q", 3)
-    _need(k, torch.bfloat16, "k", 3)
-    _need(v, torch.bfloat16, "v", 3)
-    _need(cu_seqlens_q, torch.int32, "cu_seqlens_q", 1)
-    _need(cu_seqlens_k, torch.int32, "cu_seqlens_k", 1)
-    _need(out, torch.bfloat16, "out", 3)
-    _need(lse, torch.float32, "lse", 2)
+    bf16, i32 = torch.bfloat16, torch.int32
+    dev = _cuda(q, "q")
+    pq = _ten(q, bf16, (None, None, None), dev, "q")
     T_q, H, d_qk = q.shape
-    T_k, d_v = k.shape[0], v.shape[2]
-    _shape(k, (T_k, H, d_qk), "k")
-    _shape(v, (T_k, H, d_v), "v")
-    _shape(out, (T_q, H, d_v), "out")
-    _shape(lse, (T_q, H), "lse")
-    _shape(cu_seqlens_q, (int(B) + 1,), "cu_seqlens_q")
-    _shape(cu_seqlens_k, (int(B) + 1,), "cu_seqlens_k")
-    for t, name in ((k, "k"), (v, "v"), (cu_seqlens_q, "cu_seqlens_q"),
-                    (cu_seqlens_k, "cu_seqlens_k"), (out, "out"), (lse, "lse")):
-        if t is not None and t.device != q.device:
-            raise ValueError(f"{name} must be on q's device, {q.device}")
-    st = _stream_on(stream, q.device)
-    with torch.cuda.device(q.device):
-        rc = load().dsa_window_mha_fwd(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), int(B),
-            int(max_len_q), int(max_len_k), int(T_q), int(T_k), int(H), int(d_qk), int(d_v),
-            int(window), int(sinks), float(sm_scale), _ptr(out), _ptr(lse),
-            ctypes.c_void_p(st.cuda_stream))
+    pk = _ten(k, bf16, (None, H, d_qk), dev, "k")
+    T_k = k.shape[0]
+    pv = _ten(v, bf16, (T_k, H, None), dev, "v")
+    d_v = v.shape[2]
+    po = _ten(out, bf16, (T_q, H, d_v), dev, "out")
+    pl = _ten(lse, torch.float32, (T_q, H), dev, "lse")
+    cq = _ten(cu_seqlens_q, i32, (B + 1,), dev, "cu_seqlens_q")
+    ck = _ten(cu_seqlens_k, i32, (B + 1,), dev, "cu_seqlens_k")
+    with _On(dev, stream) as st:
+        rc = load().dsa_window_mha_fwd(pq, pk, pv, cq, ck, B, max_len_q, max_len_k, T_q, T_k, H,
+                                       d_qk, d_v, window, sinks, sm_scale, po, pl, st)
     _check(rc, "dsa_window_mha_fwd")
-
-
-def _stream_on(stream, device):
-    """The torch stream a call runs on: the given one (a torch stream or a raw
-    handle), or the device's current stream."""
-    import torch
-    if stream is None:
-        return torch.cuda.current_stream(device)
-    if hasattr(stream, "cuda_stream"):
-        return stream
-    return torch.cuda.ExternalStream(int(stream), device=device)
-
-
-def _paged(kv_cache, block_table, seq_lens, **others):
-    """Checks the tensors of a call over a paged cache against each other and
-    returns the cache's arguments in the C ABI's order."""
-    import torch
-    if kv_cache.dim() != 3 or kv_cache.shape[2] != 576:
-        raise ValueError("kv_cache must be [n_pages, page_size, 576]")
-    if kv_cache.dtype != torch.bfloat16 or not kv_cache.is_cuda:
-        raise ValueError("kv_cache must be a CUDA torch.bfloat16 tensor")
-    if kv_cache.stride(2) != 1 or (kv_cache.shape[1] > 1 and kv_cache.stride(1) != 576):
-        raise ValueError("kv_cache rows must be contiguous within a page")
-    if kv_cache.shape[0] > 1 and kv_cache.stride(0) < 0:
-        raise ValueError("kv_cache pages must be in memory order")
-    _need(seq_lens, torch.int32, "seq_lens", 1)
-    B = seq_lens.shape[0]
-    tables = {"block_table": block_table}
-    tables.update((k, v) for k, v in others.items() if k.endswith("block_table"))
-    for name, t in tables.items():
-        if t.dim() != 2 or t.dtype != torch.int32 or not t.is_cuda or t.shape[0] != B:
-            raise ValueError(f"{name} must be a CUDA torch.int32 tensor [B, pages]")
-        if t.shape[1] > 1 and t.stride(1) != 1:
-            raise ValueError(f"{name} rows must be contiguous")
-    for name, t in {"block_table": block_table, "seq_lens": seq_lens, **others}.items():
-        if t is not None and t.device != kv_cache.device:
-            raise ValueError(f"{name} must be on kv_cache's device, {kv_cache.device}")
-    n_pages, page = kv_cache.shape[:2]
-    stride = kv_cache.stride(0) if n_pages > 1 else page * 576
-    return (_ptr(kv_cache), int(n_pages), int(page), int(stride), _ptr(block_table),
-            _table_ld(block_table), int(block_table.shape[1]), _ptr(seq_lens), int(B))
-
-
-def _table_ld(t):
-    return int(t.stride(0)) if t.shape[0] > 1 else int(t.shape[1])
-
-
-def _shape(t, shape, name):
-    if t is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def dsa_paged_mla_decode_workspace_size(B, H, max_len_k) -> int:
@@ -559,35 +589,22 @@ def dsa_paged_mla_decode(q, kv_cache, block_table, seq_lens, max_len_k, sm_scale
     (uint8 CUDA tensor) is allocated here, on the call's stream, when not
     given."""
     import torch
-    _need(q, torch.bfloat16, "q", 3)
-    _need(out, torch.bfloat16, "out", 3)
-    _need(lse, torch.float32, "lse", 2)
-    _need(workspace, torch.uint8, "workspace")
-    cache = _paged(kv_cache, block_table, seq_lens, q=q, out=out, lse=lse, workspace=workspace)
-    B, H, d_qk = q.shape
-    _shape(q, (seq_lens.shape[0], H, d_qk), "q")
-    _shape(out, (B, H, out.shape[2]), "out")
-    _shape(lse, (B, H), "lse")
-    st = _stream_on(stream, q.device)
-    with torch.cuda.device(q.device), torch.cuda.stream(st):
-        if workspace is None:
-            nbytes = dsa_paged_mla_decode_workspace_size(B, H, max_len_k)
-            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
-        rc = load().dsa_paged_mla_decode(
-            _ptr(q), *cache, int(max_len_k), int(H), int(d_qk), int(out.shape[2]), int(window),
-            int(sinks), float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace),
-            int(workspace.numel()), ctypes.c_void_p(st.cuda_stream))
+    cache, dev = _cache(kv_cache, block_table, seq_lens)
+    B = cache[-1]
+    pq = _ten(q, torch.bfloat16, (B, None, None), dev, "q")
+    _, H, d_qk = q.shape
+    po = _ten(out, torch.bfloat16, (B, H, None), dev, "out")
+    pl = _ten(lse, torch.float32, (B, H), dev, "lse")
+    pw = _ten(workspace, torch.uint8, (None,), dev, "workspace")
+    lib = load()
+    with _On(dev, stream) as st:
+        if pw is None:
+            nbytes = lib.dsa_paged_mla_decode_workspace_size(B, H, max_len_k)
+            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+            pw = workspace.data_ptr()
+        rc = lib.dsa_paged_mla_decode(pq, *cache, max_len_k, H, d_qk, out.shape[2], window, sinks,
+                                      sm_scale, po, pl, pw, workspace.numel(), st)
     _check(rc, "dsa_paged_mla_decode")
-
-
-def _rows_f32(t, B, n, name):
-    """A CUDA float32 matrix [B, >= n] with contiguous rows; its row stride."""
-    import torch
-    if t.dtype != torch.float32 or not t.is_cuda or t.dim() != 2 or t.shape[0] != B:
-        raise ValueError(f"{name} must be a CUDA torch.float32 tensor [B, entries]")
-    if t.shape[1] < n or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must have contiguous rows of at least {n} entries")
-    return int(t.stride(0)) if B > 1 else int(t.shape[1])
 
 
 def dsa_paged_attn_mass(q, kv_cache, block_table, seq_lens, lse, max_len_k, sm_scale, mass_out,
@@ -597,22 +614,19 @@ def dsa_paged_attn_mass(q, kv_cache, block_table, seq_lens, lse, max_len_k, sm_s
     (which may be mass_in); lse as dsa_paged_mla_decode wrote it for the same
     arguments (see include/dsa.h)."""
     import torch
-    _need(q, torch.bfloat16, "q", 3)
-    _need(lse, torch.float32, "lse", 2)
-    cache = _paged(kv_cache, block_table, seq_lens, q=q, lse=lse, mass_out=mass_out,
-                   mass_in=mass_in)
-    B, H, d_qk = q.shape
-    _shape(q, (seq_lens.shape[0], H, d_qk), "q")
-    _shape(lse, (B, H), "lse")
-    ld = _rows_f32(mass_out, B, int(max_len_k), "mass_out")
-    if mass_in is not None and _rows_f32(mass_in, B, int(max_len_k), "mass_in") != ld and B > 1:
+    f32 = torch.float32
+    cache, dev = _cache(kv_cache, block_table, seq_lens)
+    B = cache[-1]
+    pq = _ten(q, torch.bfloat16, (B, None, None), dev, "q")
+    _, H, d_qk = q.shape
+    pl = _ten(lse, f32, (B, H), dev, "lse")
+    po, ld = _rows(mass_out, f32, B, max_len_k, dev, "mass_out")
+    pi, ld_in = _rows(mass_in, f32, B, max_len_k, dev, "mass_in")
+    if pi is not None and ld_in != ld and B > 1:
         raise ValueError("mass_in and mass_out must have the same row stride")
-    st = _stream_on(stream, q.device)
-    with torch.cuda.device(q.device):
-        rc = load().dsa_paged_attn_mass(
-            _ptr(q), *cache, int(max_len_k), int(H), int(d_qk), int(window), int(sinks),
-            float(sm_scale), _ptr(lse), _ptr(mass_in), _ptr(mass_out), ld,
-            ctypes.c_void_p(st.cuda_stream))
+    with _On(dev, stream) as st:
+        rc = load().dsa_paged_attn_mass(pq, *cache, max_len_k, H, d_qk, window, sinks, sm_scale,
+                                        pl, pi, po, ld, st)
     _check(rc, "dsa_paged_attn_mass")
 
 
@@ -624,22 +638,17 @@ def dsa_cache_evict(kv_cache, block_table, seq_lens, mass, max_len_k, budget, si
     idx_out [B, budget] (old positions, -1 padded) and new_mass
     [B, >= budget] (optional).  See include/dsa.h."""
     import torch
-    _need(new_lens, torch.int32, "new_lens", 1)
-    _need(idx_out, torch.int32, "idx_out", 2)
-    cache = _paged(kv_cache, block_table, seq_lens, new_block_table=new_block_table, mass=mass,
-                   new_lens=new_lens, idx_out=idx_out, new_mass=new_mass)
-    B = seq_lens.shape[0]
-    _shape(new_lens, (B,), "new_lens")
-    _shape(idx_out, (B, int(budget)), "idx_out")
-    ld = _rows_f32(mass, B, int(max_len_k), "mass")
-    ld_new = 0 if new_mass is None else _rows_f32(new_mass, B, int(budget), "new_mass")
-    st = _stream_on(stream, kv_cache.device)
-    with torch.cuda.device(kv_cache.device):
-        rc = load().dsa_cache_evict(
-            *cache, int(max_len_k), _ptr(mass), ld, int(budget), int(sinks), int(recent),
-            _ptr(new_block_table), _table_ld(new_block_table), int(new_block_table.shape[1]),
-            _ptr(new_lens), _ptr(idx_out), _ptr(new_mass), ld_new,
-            ctypes.c_void_p(st.cuda_stream))
+    i32, f32 = torch.int32, torch.float32
+    cache, dev = _cache(kv_cache, block_table, seq_lens)
+    B = cache[-1]
+    pm, ld = _rows(mass, f32, B, max_len_k, dev, "mass")
+    pt, ld_t = _rows(new_block_table, i32, B, 1, dev, "new_block_table")
+    pn = _ten(new_lens, i32, (B,), dev, "new_lens")
+    pi = _ten(idx_out, i32, (B, budget), dev, "idx_out")
+    po, ld_o = _rows(new_mass, f32, B, budget, dev, "new_mass")
+    with _On(dev, stream) as st:
+        rc = load().dsa_cache_evict(*cache, max_len_k, pm, ld, budget, sinks, recent, pt, ld_t,
+                                    new_block_table.shape[1], pn, pi, po, ld_o, st)
     _check(rc, "dsa_cache_evict")
 
 

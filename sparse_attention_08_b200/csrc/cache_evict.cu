@@ -38,6 +38,8 @@ constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kClusterC = 8;
+constexpr int kAhead = 16;                // loads in flight per thread while a row is read
+constexpr int kGo = 4;                   // keys per step of the passes over shared memory
 constexpr int kOneCta = 8192;            // rows of at most this many entries take one CTA
 
 struct Params {
@@ -63,13 +65,34 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+}
+
+// Sum of the lanes below `upto` (v: one value per lane), the same in every lane.
+__device__ __forceinline__ uint32_t sum_below(uint32_t v, int upto) {
+  return __reduce_add_sync(0xffffffffu, static_cast<int>(threadIdx.x % 32) < upto ? v : 0u);
+}
+
+// Sum of the lanes below this one.
+__device__ __forceinline__ uint32_t sums_above(uint32_t v) {
+  uint32_t inc = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const uint32_t x = __shfl_up_sync(0xffffffffu, inc, d);
+    if (static_cast<int>(threadIdx.x % 32) >= d) inc += x;
+  }
+  return inc - v;
+}
+
 template <int C>
 __global__ void __launch_bounds__(kThreads, 1) select_kernel(const Params P) {
   extern __shared__ uint32_t keys[];     // [kWarps * wseg]
   __shared__ uint32_t hist[2][kBins];
   __shared__ uint32_t wsum[kWarps], weq[kWarps];
+  __shared__ alignas(8) uint32_t groups[2][kBins / 32];   // by pass, as hist
   __shared__ uint32_t found[2];          // the pass's bin, the rank left inside it
-  __shared__ uint32_t xch[2];            // this CTA's entries above T, equal to T
+  __shared__ alignas(8) uint32_t xch[2];            // this CTA's entries above T, equal to T
   const int rank = C == 1 ? 0 : static_cast<int>(cg::this_cluster().block_rank());
   const int b = blockIdx.x / C;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -78,8 +101,12 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const Params P) {
   int32_t* idx = P.idx + static_cast<int64_t>(b) * P.budget;
   float* nm = P.new_mass ? P.new_mass + static_cast<int64_t>(b) * P.ld_new : nullptr;
   const int kept = min(n, P.budget);
+  grid_release();
   auto sync_all = [&]() {
     if (C == 1) __syncthreads(); else cg::this_cluster().sync();
+  };
+  auto remote = [&](uint32_t* p, int q) -> const uint32_t* {
+    return C == 1 ? p : cg::this_cluster().map_shared_rank(p, (rank + q) % C);
   };
   if (rank == 0 && tid == 0) {
     P.new_lens[b] = kept;
@@ -105,66 +132,93 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const Params P) {
   const int len = min(max(m - w0, 0), P.wseg);
   uint32_t* mine = keys + warp * P.wseg;
   const float* src = row + lo + w0;
-  for (int i = lane; i < len; i += 32 * 8) {
-    float x[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) x[u] = i + 32 * u < len ? __ldg(src + i + 32 * u) : 0.f;
-#pragma unroll
-    for (int u = 0; u < 8; ++u)
-      if (i + 32 * u < len) mine[i + 32 * u] = order_key(x[u]);
-  }
   for (int i = tid; i < 2 * kBins; i += kThreads) (&hist[0][0])[i] = 0;
   __syncthreads();
+  // one warp's 32 keys into a histogram; lanes that agree (stretches of equal
+  // totals) count once
+  auto count = [&](uint32_t* h, bool in, uint32_t d) {
+    const uint32_t on = __ballot_sync(0xffffffffu, in);
+    if (on == 0) return;
+    const int lead = __ffs(on) - 1;
+    const uint32_t first = __shfl_sync(0xffffffffu, d, lead);
+    if (__all_sync(0xffffffffu, !in || d == first)) {
+      if (lane == lead) atomicAdd(h + d, static_cast<uint32_t>(__popc(on)));
+    } else if (in) {
+      atomicAdd(h + d, 1u);
+    }
+  };
+  // the row is read once, and counted by its top 11 bits as it arrives
+#pragma unroll 1
+  for (int i = lane; i - lane < len; i += 32 * kAhead) {
+    float x[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) x[u] = i + 32 * u < len ? __ldg(src + i + 32 * u) : 0.f;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const bool in = i + 32 * u < len;
+      const uint32_t k = order_key(x[u]);
+      if (in) mine[i + 32 * u] = k;
+      count(hist[0], in, k >> 21);
+    }
+  }
 
   uint32_t want = static_cast<uint32_t>(room), prefix = 0;
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    const int up = pass == 0 ? 32 : pass == 1 ? 21 : 10;      // bits above the digit's
+    const int up = pass == 1 ? 21 : 10;      // where the bits above the digit start
     const uint32_t mask = pass == 2 ? 1023u : 2047u;
     uint32_t* h = hist[pass & 1];
-    for (int i = lane; i - lane < len; i += 32) {
-      const uint32_t k = i < len ? mine[i] : 0u;
-      const bool in = i < len && (pass == 0 || (k >> up) == prefix);
-      const uint32_t on = __ballot_sync(0xffffffffu, in);
-      if (on == 0) continue;
-      const uint32_t d = (k >> shift) & mask;
-      // lanes that agree (stretches of equal totals) count once
-      const int lead = __ffs(on) - 1;
-      const uint32_t first = __shfl_sync(0xffffffffu, d, lead);
-      if (__all_sync(0xffffffffu, !in || d == first)) {
-        if (lane == lead) atomicAdd(h + d, static_cast<uint32_t>(__popc(on)));
-      } else if (in) {
-        atomicAdd(h + d, 1u);
-      }
+    uint32_t* group = groups[pass & 1];
+#pragma unroll 1
+    for (int i = lane; pass > 0 && i - lane < len; i += 32 * kGo) {
+      uint32_t k[kGo];
+#pragma unroll
+      for (int u = 0; u < kGo; ++u) k[u] = i + 32 * u < len ? mine[i + 32 * u] : 0u;
+#pragma unroll
+      for (int u = 0; u < kGo; ++u)
+        count(h, i + 32 * u < len && (k[u] >> up) == prefix, (k[u] >> shift) & mask);
+    }
+    __syncthreads();
+    // The bin of the want-th largest, in two steps from the top: the bins in 64
+    // groups of 32, then the 32 bins of the group that holds it.  Both steps
+    // read the other CTAs' counts once, 64 and 32 words each, instead of all
+    // their 2048 (which took 2 us a pass).
+    {
+      const uint32_t v0 = __reduce_add_sync(0xffffffffu, h[64 * warp + lane]);
+      const uint32_t v1 = __reduce_add_sync(0xffffffffu, h[64 * warp + 32 + lane]);
+      if (lane == 0) *reinterpret_cast<uint2*>(group + 2 * warp) = make_uint2(v0, v1);
     }
     sync_all();
-    // the bin of the want-th largest: thread t sums bins 2047 - 2t and 2046 - 2t
-    // over the cluster, then a block scan from the top
-    uint32_t c0 = 0, c1 = 0;
-    for (int q = 0; q < C; ++q) {
-      const uint32_t* o = C == 1 ? h : cg::this_cluster().map_shared_rank(h, (rank + q) % C);
-      const uint2 x = *reinterpret_cast<const uint2*>(o + kBins - 2 - 2 * tid);
-      c0 += x.y;
-      c1 += x.x;
-    }
-    uint32_t inc = c0 + c1;
+    if (warp == 0) {
+      // lane l: groups 63 - 2l and 62 - 2l, summed over the cluster
+      uint32_t c0 = 0, c1 = 0;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const uint32_t v = __shfl_up_sync(0xffffffffu, inc, d);
-      if (lane >= d) inc += v;
-    }
-    if (lane == 31) wsum[warp] = inc;
-    __syncthreads();
-    uint32_t before = 0;
-    for (int w = 0; w < warp; ++w) before += wsum[w];
-    before += inc - c0 - c1;
-    if (before < want && want <= before + c0) {
-      found[0] = kBins - 1 - 2 * tid;
-      found[1] = want - before;
-    } else if (before + c0 < want && want <= before + c0 + c1) {
-      found[0] = kBins - 2 - 2 * tid;
-      found[1] = want - before - c0;
+      for (int q = 0; q < C; ++q) {
+        const uint2 x = *reinterpret_cast<const uint2*>(remote(group, q) + 62 - 2 * lane);
+        c0 += x.y;
+        c1 += x.x;
+      }
+      uint32_t before = sums_above(c0 + c1);
+      uint32_t g = 0, left = 0;
+      bool here = before < want && want <= before + c0 + c1;
+      if (here) {
+        const bool second = want > before + c0;
+        g = 63 - 2 * lane - (second ? 1 : 0);
+        left = want - before - (second ? c0 : 0);
+      }
+      int who = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+      g = __shfl_sync(0xffffffffu, g, who);
+      left = __shfl_sync(0xffffffffu, left, who);
+      // lane l: bin 32 g + 31 - l
+      uint32_t c = 0;
+#pragma unroll
+      for (int q = 0; q < C; ++q) c += remote(h, q)[32 * g + 31 - lane];
+      before = sums_above(c);
+      if (before < left && left <= before + c) {
+        found[0] = 32 * g + 31 - lane;
+        found[1] = left - before;
+      }
     }
     __syncthreads();
     prefix = (prefix << (pass == 2 ? 10 : 11)) | found[0];
@@ -177,51 +231,60 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const Params P) {
   const uint32_t T = prefix;             // keep every key above T and the first `want` equal ones
 
   uint32_t gt = 0, eq = 0;
-  for (int i = 0; i < len; i += 32) {
-    const uint32_t k = i + lane < len ? mine[i + lane] : 0u;
-    const bool ok = i + lane < len;
-    gt += __popc(__ballot_sync(0xffffffffu, ok && k > T));
-    eq += __popc(__ballot_sync(0xffffffffu, ok && k == T));
+#pragma unroll 1
+  for (int i = lane; i - lane < len; i += 32 * kGo) {
+#pragma unroll
+    for (int u = 0; u < kGo; ++u) {
+      const bool ok = i + 32 * u < len;
+      const uint32_t k = ok ? mine[i + 32 * u] : 0u;
+      gt += __popc(__ballot_sync(0xffffffffu, ok && k > T));
+      eq += __popc(__ballot_sync(0xffffffffu, ok && k == T));
+    }
   }
   if (lane == 0) {
     wsum[warp] = gt;
     weq[warp] = eq;
   }
   __syncthreads();
-  uint32_t bg = 0, be = 0, tg = 0, te = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) {
-      bg += wsum[w];
-      be += weq[w];
+  uint32_t bg = sum_below(wsum[lane], warp), be = sum_below(weq[lane], warp);
+  if (C > 1) {
+    if (tid == kThreads - 1) {
+      xch[0] = bg + gt;
+      xch[1] = be + eq;
     }
-    tg += wsum[w];
-    te += weq[w];
-  }
-  if (tid == 0) {
-    xch[0] = tg;
-    xch[1] = te;
-  }
-  sync_all();
-  for (int q = 0; q < rank; ++q) {
-    const uint32_t* o = cg::this_cluster().map_shared_rank(xch, q);
-    bg += o[0];
-    be += o[1];
+    sync_all();
+#pragma unroll
+    for (int q = 0; q < C; ++q) {
+      const uint2 o = *reinterpret_cast<const uint2*>(cg::this_cluster().map_shared_rank(xch, q));
+      if (q < rank) {
+        bg += o.x;
+        be += o.y;
+      }
+    }
   }
   const uint32_t lt = (1u << lane) - 1;
-  for (int i = 0; i < len; i += 32) {
-    const bool ok = i + lane < len;
-    const uint32_t k = ok ? mine[i + lane] : 0u;
-    const uint32_t mg = __ballot_sync(0xffffffffu, ok && k > T);
-    const uint32_t me = __ballot_sync(0xffffffffu, ok && k == T);
-    const uint32_t g = bg + __popc(mg & lt), e = be + __popc(me & lt);
-    if (ok && (k > T || (k == T && e < want))) {
-      const int s = lo + w0 + i + lane;
-      const int64_t j = P.sinks + static_cast<int64_t>(g) + min(e, want);
-      idx[j] = s;
-      if (nm) nm[j] = __ldg(row + s);
+#pragma unroll 1
+  for (int i = lane; i - lane < len; i += 32 * kGo) {
+    uint32_t k[kGo];
+#pragma unroll
+    for (int u = 0; u < kGo; ++u) k[u] = i + 32 * u < len ? mine[i + 32 * u] : 0u;
+#pragma unroll
+    for (int u = 0; u < kGo; ++u) {
+      const bool ok = i + 32 * u < len;
+      const uint32_t mg = __ballot_sync(0xffffffffu, ok && k[u] > T);
+      const uint32_t me = __ballot_sync(0xffffffffu, ok && k[u] == T);
+      const uint32_t g = bg + __popc(mg & lt), e = be + __popc(me & lt);
+      if (ok && (k[u] > T || (k[u] == T && e < want))) {
+        const int s = lo + w0 + i + 32 * u;
+        const int64_t j = P.sinks + static_cast<int64_t>(g) + min(e, want);
+        idx[j] = s;
+        // the total itself, from its key unless that stands for several
+        if (nm)
+          nm[j] = k[u] == 0xFFFFFFFFu || k[u] == 0x80000000u ? __ldg(row + s) : key_value(k[u]);
+      }
+      bg += __popc(mg);
+      be += __popc(me);
     }
-    bg += __popc(mg);
-    be += __popc(me);
   }
   // nobody's shared memory goes away while another CTA may still read it
   if (C > 1) cg::this_cluster().sync();
@@ -229,10 +292,11 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const Params P) {
 
 // Four kept latents per warp: 288 pieces of 16 bytes, nine per lane.
 constexpr int kMoveRows = 4;
-__global__ void __launch_bounds__(256) move_kernel(const Params P, uint8_t* pool, int groups) {
+__global__ void __launch_bounds__(256, 4) move_kernel(Params P, uint8_t* pool, int groups) {
   const int lane = threadIdx.x % 32;
   const int64_t all = static_cast<int64_t>(groups) * P.c.B;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * 8;
+  grid_wait();
   for (int64_t t = blockIdx.x * 8ll + threadIdx.x / 32; t < all; t += stride) {
     const int b = static_cast<int>(t / groups);
     const int j = static_cast<int>(t % groups) * kMoveRows + lane;
@@ -316,9 +380,8 @@ cudaError_t launch_cache_evict(const CacheEvictArgs& a, DevErr err, cudaStream_t
   if (groups == 0) return cudaSuccess;
   const int64_t ctas = (static_cast<int64_t>(groups) * P.c.B + 7) / 8;
   const int64_t most = static_cast<int64_t>(a.num_sms) * 16;
-  move_kernel<<<static_cast<unsigned>(ctas < most ? ctas : most), 256, 0, s>>>(
-      P, const_cast<uint8_t*>(P.c.pool), groups);
-  return cudaGetLastError();
+  return launch_after(move_kernel, dim3(static_cast<unsigned>(ctas < most ? ctas : most)), 256, 0,
+                      s, P, const_cast<uint8_t*>(P.c.pool), groups);
 }
 
 }  // namespace dsa

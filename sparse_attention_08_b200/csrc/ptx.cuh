@@ -476,6 +476,35 @@ constexpr uint32_t kFmtBF16 = 1;
 constexpr uint32_t kFmtE4M3 = 0;
 
 // ---------------------------------------------------------------------------
+// Programmatic dependent launch: a kernel launched with launch_after may start
+// while the one before it on the stream still runs, and must call grid_wait
+// (which returns once that one has finished and its writes are visible) before
+// it touches anything the other writes.  grid_release lets it start.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void grid_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void grid_release() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <typename... Args>
+cudaError_t launch_after(void (*kernel)(Args...), dim3 grid, unsigned threads, size_t smem,
+                         cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// ---------------------------------------------------------------------------
 // Small numeric helpers.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float fast_exp2(float x) {

@@ -25,7 +25,7 @@
 //  warps 4..11 two warpgroups, one per query tile, a thread one row: P over
 //              the scores' own columns, no exchange between threads.  The
 //              running maximum of the tile before serves as the exponentials'
-//              reference; only where a score exceeds it by more than 2^8 is the
+//              reference; only where a score exceeds it by more than 2^32 is the
 //              tile's maximum taken first and O rescaled.
 // TMEM: S (and P) at columns 0 and 128, O at 256 and 384.
 //
@@ -65,7 +65,13 @@ constexpr uint32_t kColO = 256;
 constexpr uint32_t kIdescS = instr_desc(kFmtBF16, kFmtBF16, 0, 0, kBM, kBN);
 constexpr uint32_t kIdescPV = instr_desc(kFmtBF16, kFmtBF16, 0, 1, kBM, kDv);
 constexpr uint32_t kIdescPV64 = instr_desc(kFmtBF16, kFmtBF16, 0, 1, kBM, 64);
-constexpr float kSlack = 8.0f;                         // log2 units above the reference
+// How far (log2 units) a score may lie above its row's reference before the
+// reference is moved.  P is bf16 and O fp32, with 8-bit exponents both: a weight
+// of 2^32 loses nothing against one of 1 (values of up to 2^70 times 2^32 and a
+// sum over 2^24 keys stay finite).  A slack of 2^8 was exceeded in every other
+// tile by some row whose first tile held a few keys of its window only, and
+// each time cost its warp the tile twice.
+constexpr float kSlack = 32.0f;
 
 static_assert(kSmem <= 232448, "shared memory budget");
 
