@@ -69,21 +69,37 @@ __device__ __forceinline__ Seen seen_of(const Cache& c, int len) {
 
 // A warp's wait in which every lane polls: the verdict needs no broadcast,
 // which shortens the wake-up by about 100 cycles against warp_wait.  The waiting
-// loop is out of line to keep the roles' loops short.
+// loop is out of line to keep the roles' loops short, and looks at the launch's
+// error word and the clock only every 1024 polls: the load of the word takes as
+// long as a dozen polls, during which a finished phase goes unseen.
 static __device__ __noinline__ bool wait_loop(uint32_t bar, uint32_t parity, unsigned* word,
                                               unsigned gen, uint64_t limit_ns) {
   DevErr e;
   e.word = word;
   e.gen = gen;
-  e.inject = 0;
-  e.limit_ns = limit_ns;
-  return mbar_wait(bar, parity, e);
+  uint64_t t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 1023u) == 0) {
+      if (launch_failed(e)) return false;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > limit_ns) {
+        raise_error(e, kErrTimeout);
+        return false;
+      }
+    }
+  }
 }
 
 __device__ __forceinline__ bool all_wait(uint32_t bar, uint32_t parity, const DevErr& e) {
   const bool ok = mbar_try_wait(bar, parity) || wait_loop(bar, parity, e.word, e.gen, e.limit_ns);
   return __all_sync(0xffffffffu, ok);
 }
+
+// A value that all lanes hold alike, in a form the compiler knows to be so: MMA
+// operands made from it stay in uniform registers.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // Sum over the warp, the same in every lane.
 __device__ __forceinline__ int warp_sum(int v) {

@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   const Start start = find_start(P.c, piece, P.pieces, 1, kWarps, scratch, P.err);
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
   grid_release();
   if (blockIdx.x == 0 && threadIdx.x == 0) P.plan[P.c.B] = start.per;
   Walk w(P.c, start, 1);

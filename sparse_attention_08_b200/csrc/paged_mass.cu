@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   const Start start = find_start(P.c, blockIdx.x, P.pieces, 0, kWarps, scratch, P.err);
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
   Walk w(P.c, start, 0);
 
   if (warp < 2) {

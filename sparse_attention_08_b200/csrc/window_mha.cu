@@ -10,9 +10,8 @@
 // A persistent grid of one CTA per SM.  A work item is a pair of 128-query
 // tiles of one sequence and head; it walks the 128-key tiles that hold a key some row
 // of the pair sees (the first tokens' tiles, then the window's).  The two
-// query tiles have their own score and output accumulators in TMEM, and the
-// MMA warp alternates between them, so the softmax of one runs under the
-// products of the other:
+// query tiles have their own score and output accumulators in TMEM and an MMA
+// warp each, so the softmax of one runs under the products of the other:
 //
 //   ... P V (tile 0, j)  S (tile 0, j+1)  P V (tile 1, j)  S (tile 1, j+1) ...
 //
@@ -20,8 +19,9 @@
 //              columns) through one ring of eight; a key tile is three boxes,
 //              a value tile two, and a box is reloaded as soon as both query
 //              tiles are done with it;
-//  warp 1      MMA issuer: S = Q K^T (12 MMAs, M128 N128 K16), O += P V (8
-//              MMAs, P read from TMEM, V MN-major from shared memory);
+//  warps 1, 2  MMA issuers, one per query tile: S = Q K^T (12 MMAs, M128 N128
+//              K16), O += P V (8 MMAs, P read from TMEM, V MN-major from shared
+//              memory);
 //  warps 4..11 two warpgroups, one per query tile, a thread one row: P over
 //              the scores' own columns, no exchange between threads.  The
 //              running maximum of the tile before serves as the exponentials'
@@ -45,6 +45,7 @@ namespace {
 using paged::all_wait;
 using paged::max3;
 using paged::tma_load_3d;
+using paged::uniform;
 
 constexpr int kBM = 128;
 constexpr int kBN = 128;
@@ -55,8 +56,8 @@ constexpr uint32_t kOffQ = 0;                          // two tiles of three box
 constexpr uint32_t kOffRing = 6 * kBox;
 constexpr uint32_t kOffBar = kOffRing + kRing * kBox;
 // barriers: full[4] (units), empty[8] (boxes), q_full[2], q_empty[2], s_full[2], p_full[2],
-// o_full[2], drain
-constexpr uint32_t kNumBars = 4 + kRing + 10 + 1;
+// o_full[2], turn[2], drain
+constexpr uint32_t kNumBars = 4 + kRing + 12 + 1;
 constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;
 constexpr uint32_t kSmem = kOffMisc + 16 + 1024;
 constexpr int kThreads = 384;
@@ -161,7 +162,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto s_full = [&](int t) { return bar0 + 8u * (8 + kRing + t); };
   auto p_full = [&](int t) { return bar0 + 8u * (10 + kRing + t); };
   auto o_full = [&](int t) { return bar0 + 8u * (12 + kRing + t); };
-  const uint32_t drain = bar0 + 8u * (14 + kRing);
+  auto turn = [&](int t) { return bar0 + 8u * (14 + kRing + t); };
+  const uint32_t drain = bar0 + 8u * (16 + kRing);
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + kOffMisc);
 
   const int warp = threadIdx.x / 32;
@@ -169,15 +171,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 4; ++i) mbar_init(full(i), 1);
-    for (int i = 0; i < kRing; ++i) mbar_init(empty(i), 1);
+    for (int i = 0; i < kRing; ++i) mbar_init(empty(i), 2);
     for (int t = 0; t < 2; ++t) {
       mbar_init(q_full(t), 1);
       mbar_init(q_empty(t), 1);
       mbar_init(s_full(t), 1);
       mbar_init(p_full(t), 4);
       mbar_init(o_full(t), 1);
+      mbar_init(turn(t), 1);
     }
-    mbar_init(drain, 1);
+    mbar_init(drain, 2);
     fence_barrier_init();
     tma_prefetch_desc(&tq);
     tma_prefetch_desc(&tk);
@@ -190,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA
@@ -245,134 +248,115 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (u < unit || box > 0) mbar_wait_drain(full(u), (u / 4) & 1, P.err);
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp < 3) {
     // ------------------------------------------------------------ MMA
-    const uint64_t dQ0 = smem_desc(sbase + kOffQ, 16, 1024, kSwizzle128B);
+    // Warp 1 issues for query tile 0, warp 2 for tile 1, in turns: P V of one
+    // key tile and S of the next, then the other query tile's.  The turns keep
+    // the two tiles half a step apart, so that one's softmax runs under the
+    // other's products (left to themselves the two fall into step: both softmaxes
+    // at once, then all the products: 5500 against 4000 cycles).  A single issuer
+    // for both tiles loses about 800 cycles a step to its own waits.
+    const int t = static_cast<int>(uniform(warp - 1));
+    const uint32_t sc = tmem + 128u * t, oc = tmem + kColO + 128u * t;
+    const uint64_t dQ = smem_desc(sbase + kOffQ + 3 * t * kBox, 16, 1024, kSwizzle128B);
     const uint64_t dR = smem_desc(sbase + kOffRing, 16, 1024, kSwizzle128B);
-    // a value box: 64 of the 128 dims, MN-major
+    // a value tile: two boxes of 64 dims, MN-major
     const uint64_t dV = smem_desc(sbase + kOffRing, kBox, 1024, kSwizzle128B);
-    // phases of p_full and q_full: bit t (in registers, not in an array)
-    uint32_t box = 0, unit = 0, ns = 0, nq = 0;
+    uint32_t box = 0, unit = 0, ns = 0, nq = 0, turns = 0;
     bool ok = true;
 #pragma unroll 1
     for (int64_t it = blockIdx.x; ok && it < P.items; it += gridDim.x) {
       const Item x = item_of(P, it);
       if (x.tiles == 0) continue;
-      const Rows r0(P, x, 0), r1(P, x, 1);
-      auto needs = [&](int t, int i) -> bool {
-        const int j = x.key_tile(i);
-        return t == 0 ? r0.any(P, j) : x.tiles > 1 && r1.any(P, j);
-      };
-      // the query tiles' last key tiles
-      int last0 = x.n - 1, last1 = x.n - 1;
-      while (last0 > 0 && !needs(0, last0)) --last0;
-      while (x.tiles > 1 && last1 > 0 && !needs(1, last1)) --last1;
-      uint32_t begun = 0;         // bit t: O of tile t holds something
-      // S of query tile t with the key tile in the ring at box kb
-      auto scores = [&](int t, int i, uint32_t kb) {
-        if (elect_one()) {
-#pragma unroll
-          for (int c = 0; c < 3; ++c) {
-            const uint64_t a = dQ0 + (((3 * t + c) * kBox) >> 4);
-            const uint64_t b = dR + ((((kb + c) & (kRing - 1)) * kBox) >> 4);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_f16(tmem + 128u * t, a + ((kk * 32) >> 4), b + ((kk * 32) >> 4), kIdescS,
-                      (c | kk) != 0 ? 1u : 0u);
-          }
-          mma_commit(s_full(t));
-          if (i == (t ? last1 : last0)) mma_commit(q_empty(t));
-        }
-        __syncwarp();
-      };
-      // O += P V of query tile t with the value tile at box vb
-      auto values = [&](int t, int i, uint32_t vb) {
-        if (elect_one()) {
-          const uint32_t more = (begun >> t) & 1;
-          const uint32_t p = tmem + 128u * t, o = tmem + kColO + 128u * t;
-          const uint64_t b0 = dV + (((vb & (kRing - 1)) * kBox) >> 4);
-          if ((vb & (kRing - 1)) != kRing - 1) {
-#pragma unroll
-            for (int kk = 0; kk < kBN / 16; ++kk)
-              mma_f16_ts(o, p + 8u * kk, b0 + ((kk * 2048) >> 4), kIdescPV, kk > 0 ? 1u : more);
-          } else {
-            // one value tile in eight wraps around the ring's end: its two
-            // 64-dim boxes are not neighbours, and take an MMA each
-#pragma unroll
-            for (int kk = 0; kk < kBN / 16; ++kk) {
-              mma_f16_ts(o, p + 8u * kk, b0 + ((kk * 2048) >> 4), kIdescPV64, kk > 0 ? 1u : more);
-              mma_f16_ts(o + 64u, p + 8u * kk, dV + ((kk * 2048) >> 4), kIdescPV64, kk > 0 ? 1u : more);
-            }
-          }
-          if (i == (t ? last1 : last0)) mma_commit(o_full(t));
-        }
-        begun |= 1u << t;
-        __syncwarp();
-      };
-      auto free_boxes = [&](uint32_t b, int n) {
-        if (elect_one())
-          for (int c = 0; c < n; ++c) mma_commit(empty(b + c));
-        __syncwarp();
-      };
-      // the first key tile
-      for (int t = 0; ok && t < x.tiles; ++t) {
-        ok = all_wait(q_full(t), (nq >> t) & 1, P.err);
-        nq ^= 1u << t;
+      const Rows rr(P, x, t);
+      const bool mine = t < x.tiles;
+      auto needs = [&](int i) -> bool { return mine && rr.any(P, x.key_tile(i)); };
+      int last = x.n - 1;         // the tile's last key tile
+      while (mine && last > 0 && !needs(last)) --last;
+      if (mine) {
+        ok = all_wait(q_full(t), nq & 1, P.err);
+        ++nq;
       }
-      ok = ok && all_wait(full(unit), (unit / 4) & 1, P.err);
-      if (!ok) break;
-      tc_fence_after();
-      if (needs(0, 0)) scores(0, 0, box);
-      if (needs(1, 0)) scores(1, 0, box);
-      free_boxes(box, 3);
-      box += 3;
-      ++unit;
+      uint32_t more = 0;          // 1: O holds something
+      // (i = -1: only the scores of the first key tile)
 #pragma unroll 1
-      for (int i = 0; ok && i < x.n; ++i) {
-        const uint32_t vb = box, kb = box + 2;
-        const bool more = i + 1 < x.n;
-        ok = all_wait(full(unit), (unit / 4) & 1, P.err);
-        if (!ok) break;
-        // value rows past the sequence are another's (or unwritten memory):
-        // their weights are 0, and so must they be (0 * NaN is not)
-        const int rem = x.len_k - x.key_tile(i) * kBN;
-        if (rem < kBN && x.ck + x.len_k < P.total_k) {
-          for (int e = rem * 8 + lane; e < kBN * 8; e += 32) {
-            const uint32_t o = (e >> 3) * 128 + (e & 7) * 16;
-            *reinterpret_cast<uint4*>(smem + kOffRing + (vb & (kRing - 1)) * kBox + o) = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(smem + kOffRing + ((vb + 1) & (kRing - 1)) * kBox + o) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        ++unit;
-        bool have_k = false;
+      for (int i = -1; ok && i < x.n; ++i, ++turns) {
+        const bool pv = i >= 0 && needs(i), sn = i + 1 < x.n && needs(i + 1);
+        const uint32_t vb = uniform(box), kb = uniform(box + (i >= 0 ? 2 : 0));
+        if (i >= 0) {
+          ok = all_wait(full(unit), (unit / 4) & 1, P.err);
+          if (!ok) break;
+          ++unit;
+          // value rows past the sequence are another's (or unwritten memory):
+          // their weights are 0, and so must they be (0 * NaN is not)
+          const int rem = x.len_k - x.key_tile(i) * kBN;
+          if (pv && rem < kBN && x.ck + x.len_k < P.total_k) {
 #pragma unroll 1
-        for (int t = 0; ok && t < x.tiles; ++t) {
-          if (needs(t, i)) {
-            ok = all_wait(p_full(t), (ns >> t) & 1, P.err);
-            if (!ok) break;
-            ns ^= 1u << t;
-            tc_fence_after();
-            values(t, i, vb);
-          }
-          if (t + 1 == x.tiles) free_boxes(vb, 2);
-          if (more) {
-            if (!have_k) {
-              ok = all_wait(full(unit), (unit / 4) & 1, P.err);
-              if (!ok) break;
-              tc_fence_after();
-              have_k = true;
+            for (int e = rem * 8 + lane; e < kBN * 8; e += 32) {
+              const uint32_t o = (e >> 3) * 128 + (e & 7) * 16;
+              *reinterpret_cast<uint4*>(smem + kOffRing + (vb & (kRing - 1)) * kBox + o) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(smem + kOffRing + ((vb + 1) & (kRing - 1)) * kBox + o) = make_uint4(0, 0, 0, 0);
             }
-            if (needs(t, i + 1)) scores(t, i + 1, kb);
-            if (t + 1 == x.tiles) free_boxes(kb, 3);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (pv) {
+            ok = all_wait(p_full(t), ns & 1, P.err);
+            if (!ok) break;
+            ++ns;
           }
         }
-        box += 2;
-        if (more) {
-          box += 3;
+        if (i + 1 < x.n) {
+          ok = all_wait(full(unit), (unit / 4) & 1, P.err);
+          if (!ok) break;
           ++unit;
         }
+        ok = all_wait(turn(t), (turns & 1) ^ (t == 0 ? 1u : 0u), P.err);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          if (pv) {
+            const uint64_t b0 = dV + (((vb & (kRing - 1)) * kBox) >> 4);
+            if ((vb & (kRing - 1)) != kRing - 1) {
+#pragma unroll
+              for (int kk = 0; kk < kBN / 16; ++kk)
+                mma_f16_ts(oc, sc + 8u * kk, b0 + ((kk * 2048) >> 4), kIdescPV, kk > 0 ? 1u : more);
+            } else {
+              // one value tile in eight wraps around the ring's end: its two
+              // boxes are not neighbours, and take an MMA each
+#pragma unroll 1
+              for (int kk = 0; kk < kBN / 16; ++kk) {
+                mma_f16_ts(oc, sc + 8u * kk, b0 + ((kk * 2048) >> 4), kIdescPV64, kk > 0 ? 1u : more);
+                mma_f16_ts(oc + 64u, sc + 8u * kk, dV + ((kk * 2048) >> 4), kIdescPV64, kk > 0 ? 1u : more);
+              }
+            }
+            if (i == last) mma_commit(o_full(t));
+            mma_commit(empty(vb));
+            mma_commit(empty(vb + 1));
+          }
+          if (sn) {
+#pragma unroll
+            for (int c = 0; c < 3; ++c) {
+              const uint64_t b = dR + ((((kb + c) & (kRing - 1)) * kBox) >> 4);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_f16(sc, dQ + ((c * kBox + kk * 32) >> 4), b + ((kk * 32) >> 4), kIdescS,
+                        (c | kk) != 0 ? 1u : 0u);
+            }
+            mma_commit(s_full(t));
+            if (i + 1 == last) mma_commit(q_empty(t));
+            mma_commit(empty(kb));
+            mma_commit(empty(kb + 1));
+            mma_commit(empty(kb + 2));
+          }
+          mbar_arrive(turn(t ^ 1));
+        }
+        __syncwarp();
+        if (pv) more = 1;
+        // boxes that this query tile has no use for
+        if (i >= 0 && !pv && lane < 2) mbar_arrive(empty(vb + lane));
+        if (i + 1 < x.n && !sn && lane < 3) mbar_arrive(empty(kb + lane));
+        box = kb + (i + 1 < x.n ? 3 : 0);
       }
     }
     mma_commit_warp(drain);
