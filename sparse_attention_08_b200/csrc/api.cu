@@ -351,7 +351,9 @@ dsa_status_t dsa_window_mha_fwd(const void* q, const void* k, const void* v,
     return DSA_ERR_UNSUPPORTED;
   if (!(sm_scale > 0.f) || sm_scale != sm_scale) return DSA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out)) return DSA_ERR_ALIGNMENT;
-  if (total_q >= (int64_t(1) << 31) || total_k >= (int64_t(1) << 31)) return DSA_ERR_UNSUPPORTED;
+  if (total_q >= (int64_t(1) << 31) || total_k >= (int64_t(1) << 31) ||
+      static_cast<int64_t>(B) * ((max_len_q + 255) / 256) >= (int64_t(1) << 30) / H)
+    return DSA_ERR_UNSUPPORTED;
   if (total_q == 0 || B == 0) return DSA_OK;
   if (total_k == 0) return DSA_ERR_INVALID_ARG;
   DeviceInfo* dev = nullptr;

@@ -243,12 +243,6 @@ __device__ __forceinline__ Box box_of(const Cache& c, const Seen& k, int b, int 
   return x;
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
 // Sums (or maxima) of 16 columns over the lanes of a warp: lanes i and i + 16
 // end with column i's, in 16 shuffles.
 template <bool kMax>

@@ -76,7 +76,7 @@ constexpr uint32_t kColO = 0;                         // + 64 * (dims / 128)
 constexpr uint32_t kColS = 256;
 constexpr uint32_t kIdescS = instr_desc(kFmtBF16, kFmtBF16, 0, 0, 128, kHeads);
 constexpr uint32_t kIdescO = instr_desc(kFmtBF16, kFmtBF16, 1, 1, 128, kHeads);
-constexpr float kSlack = 32.0f;                       // log2 units above the reference
+constexpr float kMost = 4294967296.f;                 // 2^32: largest sum of a key's weights over the references
 constexpr float kNoRef = -1e30f;                      // no score yet: any finite one is above
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -330,13 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!bad) {
           tc_fence_after();
           load();
-          if (i > w.i0) {
-            shift();
-            float top = -INFINITY;
-#pragma unroll
-            for (int e = 0; e < kWide / 2; ++e) top = max3(top, y[e].x, y[e].y);
-            over = top > kSlack;
-          }
+          if (i > w.i0) shift();
         }
         // the weights, in the hope that the references stand
         uint32_t pk[kWide / 2];
@@ -347,7 +341,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             pk[e] = pack_bf16x2(y[e].x, y[e].y);
           }
         };
-        if (i > w.i0) weigh();
+        if (i > w.i0 && !bad) {
+          weigh();
+          float2 all = y[0];
+#pragma unroll
+          for (int e = 1; e < kWide / 2; ++e) all = __fadd2_rn(all, y[e]);
+          over = all.x + all.y > kMost;       // (a weight above it makes the sum so)
+        }
         // one vote for all the warps; it also takes them out together when
         // a wait of one of them gave up
         if (named_bar_or(1, kSoftThreads, bad || over) || i == w.i0) {

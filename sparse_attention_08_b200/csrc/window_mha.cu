@@ -22,11 +22,11 @@
 //  warps 1, 2  MMA issuers, one per query tile: S = Q K^T (12 MMAs, M128 N128
 //              K16), O += P V (8 MMAs, P read from TMEM, V MN-major from shared
 //              memory);
-//  warps 4..11 two warpgroups, one per query tile, a thread one row: P over
-//              the scores' own columns, no exchange between threads.  The
-//              running maximum of the tile before serves as the exponentials'
-//              reference; only where a score exceeds it by more than 2^32 is the
-//              tile's maximum taken first and O rescaled.
+//  warps 4..19 two warpgroups per query tile, a thread half a row: P over the
+//              scores' own columns.  The running maximum of the tile before
+//              serves as the exponentials' reference; only where a row's weights
+//              over it add up to more than 2^32 is the tile's maximum taken
+//              first and O rescaled.
 // TMEM: S (and P) at columns 0 and 128, O at 256 and 384.
 //
 // Bound by the tensor cores: 20 MMAs of 64 cycles per tile pair of 128 x 128,
@@ -43,7 +43,6 @@ namespace dsa {
 namespace {
 
 using paged::all_wait;
-using paged::max3;
 using paged::tma_load_3d;
 using paged::uniform;
 
@@ -59,20 +58,24 @@ constexpr uint32_t kOffBar = kOffRing + kRing * kBox;
 // o_full[2], turn[2], drain
 constexpr uint32_t kNumBars = 4 + kRing + 12 + 1;
 constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;
-constexpr uint32_t kSmem = kOffMisc + 16 + 1024;
-constexpr int kThreads = 384;
+constexpr uint32_t kOffXchg = kOffMisc + 16;           // one float per row, between its two threads
+constexpr uint32_t kSmem = kOffXchg + 2 * 128 * 4 + 1024;
+constexpr int kThreads = 640;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;
 constexpr uint32_t kIdescS = instr_desc(kFmtBF16, kFmtBF16, 0, 0, kBM, kBN);
 constexpr uint32_t kIdescPV = instr_desc(kFmtBF16, kFmtBF16, 0, 1, kBM, kDv);
 constexpr uint32_t kIdescPV64 = instr_desc(kFmtBF16, kFmtBF16, 0, 1, kBM, 64);
-// How far (log2 units) a score may lie above its row's reference before the
-// reference is moved.  P is bf16 and O fp32, with 8-bit exponents both: a weight
-// of 2^32 loses nothing against one of 1 (values of up to 2^70 times 2^32 and a
-// sum over 2^24 keys stay finite).  A slack of 2^8 was exceeded in every other
-// tile by some row whose first tile held a few keys of its window only, and
-// each time cost its warp the tile twice.
-constexpr float kSlack = 32.0f;
+// A row's weights are 2^(score - reference).  P is bf16 and O fp32, with 8-bit
+// exponents both, so any reference within a factor of 2^32 or so of the row's largest
+// weight serves: it starts at 0 and is moved, to the tile's maximum, only when a
+// tile's weights add up to more than kMost, or the first ones that a row sees to less
+// than kLeast.  (Values of up to 2^70 times 2^32 and a sum over 2^24 keys stay finite; weights down
+// to 2^-94 of the first stay above the smallest normal number.)  Starting from the
+// first tile's maximum cost that tile twice, and a limit of 2^8 every other tile
+// of a row that began with a few keys of its window.
+constexpr float kMost = 4294967296.f;         // 2^32
+constexpr float kLeast = 2.3283064e-10f;      // 2^-32
 
 static_assert(kSmem <= 232448, "shared memory budget");
 
@@ -83,7 +86,7 @@ struct Params {
   int B, H;
   int pairs;                // query-tile pairs per sequence slot
   int window, sinks;        // window 0: no limit
-  int64_t items;
+  int items;
   float scale_log2;
   __nv_bfloat16* out;
   float* lse;
@@ -98,13 +101,14 @@ struct Item {
   __device__ __forceinline__ int key_tile(int i) const { return i < a ? i : w0 + (i - a); }
 };
 
-__device__ __forceinline__ Item item_of(const Params& P, int64_t i) {
+__device__ __forceinline__ Item item_of(const Params& P, uint32_t i) {
   Item x;
+  if (i >= static_cast<uint32_t>(P.items)) i = 0;    // (looked up ahead, past the last: not used)
   // the query tiles of a head are neighbours: they share its keys in L2; the
   // last ones, which may have the most keys, go first
-  const int64_t bh = i / P.pairs;
-  x.b = static_cast<int>(bh / P.H);
-  x.h = static_cast<int>(bh - static_cast<int64_t>(x.b) * P.H);
+  const uint32_t bh = i / static_cast<uint32_t>(P.pairs);
+  x.b = static_cast<int>(bh / static_cast<uint32_t>(P.H));
+  x.h = static_cast<int>(bh) - x.b * P.H;
   x.q0 = (P.pairs - 1 - static_cast<int>(i - bh * P.pairs)) * (2 * kBM);
   x.cq = __ldg(P.cu_q + x.b);
   x.ck = __ldg(P.cu_k + x.b);
@@ -176,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(q_full(t), 1);
       mbar_init(q_empty(t), 1);
       mbar_init(s_full(t), 1);
-      mbar_init(p_full(t), 4);
+      mbar_init(p_full(t), 8);
       mbar_init(o_full(t), 1);
       mbar_init(turn(t), 1);
     }
@@ -214,15 +218,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) ++unit;
     };
 #pragma unroll 1
-    for (int64_t i = blockIdx.x; ok && i < P.items; i += gridDim.x) {
+    for (int i = blockIdx.x; ok && i < P.items; i += gridDim.x) {
       const Item x = item_of(P, i);
       // (more queries than keys: there is no such sequence)
       if (x.off < 0 && x.rows > 0 && lane == 0) raise_error(P.err, kErrBounds);
       if (x.tiles == 0) continue;
-#pragma unroll 1
-      for (int t = 0; ok && t < x.tiles; ++t) {
-        ok = all_wait(q_empty(t), ((t ? nq1 : nq0) & 1) ^ 1, P.err);
-        if (!ok) break;
+      auto queries = [&](int t) {
+        ok = ok && all_wait(q_empty(t), ((t ? nq1 : nq0) & 1) ^ 1, P.err);
+        if (!ok) return;
         if (lane == 0) {
           mbar_arrive_expect_tx(q_full(t), 3 * kBox);
 #pragma unroll 1
@@ -232,11 +235,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (t) ++nq1; else ++nq0;
-      }
+      };
+      queries(0);
 #pragma unroll 1
       for (int j = 0; ok && j < x.n; ++j) {
         const int row = x.ck + x.key_tile(j) * kBN;
         load(&tk, 3, x.h, row);
+        // (query tile 1 is done with the item before later than tile 0)
+        if (j == 0 && x.tiles > 1) queries(1);
         load(&tv, 2, x.h, row);
       }
     }
@@ -264,24 +270,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t dV = smem_desc(sbase + kOffRing, kBox, 1024, kSwizzle128B);
     uint32_t box = 0, unit = 0, ns = 0, nq = 0, turns = 0;
     bool ok = true;
+    // The next item is looked up while this one's first softmax runs: at an item's
+    // end the lookup (loads, divisions, code not in the cache) cost 3000 cycles.
+    Item nx = item_of(P, blockIdx.x);
 #pragma unroll 1
-    for (int64_t it = blockIdx.x; ok && it < P.items; it += gridDim.x) {
-      const Item x = item_of(P, it);
-      if (x.tiles == 0) continue;
-      const Rows rr(P, x, t);
-      const bool mine = t < x.tiles;
-      auto needs = [&](int i) -> bool { return mine && rr.any(P, x.key_tile(i)); };
+    for (int it = blockIdx.x; ok && it < P.items;) {
+      const Item x = nx;
+      it += gridDim.x;
+      if (x.tiles == 0) {
+        nx = item_of(P, it);
+        continue;
+      }
+      const Rows mine(P, x, t), other(P, x, t ^ 1);
+      auto needs = [&](int u, int i) -> bool {
+        return u < x.tiles && (u == t ? mine : other).any(P, x.key_tile(i));
+      };
       int last = x.n - 1;         // the tile's last key tile
-      while (mine && last > 0 && !needs(last)) --last;
-      if (mine) {
+      while (t < x.tiles && last > 0 && !needs(t, last)) --last;
+      if (t < x.tiles) {
         ok = all_wait(q_full(t), nq & 1, P.err);
         ++nq;
       }
       uint32_t more = 0;          // 1: O holds something
       // (i = -1: only the scores of the first key tile)
 #pragma unroll 1
-      for (int i = -1; ok && i < x.n; ++i, ++turns) {
-        const bool pv = i >= 0 && needs(i), sn = i + 1 < x.n && needs(i + 1);
+      for (int i = -1; ok && i < x.n; ++i) {
+        const bool pv = i >= 0 && needs(t, i), sn = i + 1 < x.n && needs(t, i + 1);
+        // (a step in which the other query tile has no weights to wait for is no turn)
+        const bool both = pv && needs(t ^ 1, i);
         const uint32_t vb = uniform(box), kb = uniform(box + (i >= 0 ? 2 : 0));
         if (i >= 0) {
           ok = all_wait(full(unit), (unit / 4) & 1, P.err);
@@ -302,20 +318,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (pv) {
             ok = all_wait(p_full(t), ns & 1, P.err);
-            if (!ok) break;
             ++ns;
           }
-        }
-        if (i + 1 < x.n) {
-          ok = all_wait(full(unit), (unit / 4) & 1, P.err);
+          if (ok && both) {
+            ok = all_wait(turn(t), (turns & 1) ^ (t == 0 ? 1u : 0u), P.err);
+            ++turns;
+          }
           if (!ok) break;
-          ++unit;
-        }
-        ok = all_wait(turn(t), (turns & 1) ^ (t == 0 ? 1u : 0u), P.err);
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-          if (pv) {
+          tc_fence_after();
+          if (pv && elect_one()) {
             const uint64_t b0 = dV + (((vb & (kRing - 1)) * kBox) >> 4);
             if ((vb & (kRing - 1)) != kRing - 1) {
 #pragma unroll
@@ -334,7 +345,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_commit(empty(vb));
             mma_commit(empty(vb + 1));
           }
-          if (sn) {
+          __syncwarp();
+          if (pv) more = 1;
+          // boxes that this query tile has no use for
+          if (!pv && lane < 2) mbar_arrive(empty(vb + lane));
+        }
+        if (i + 1 < x.n) {
+          ok = all_wait(full(unit), (unit / 4) & 1, P.err);
+          if (!ok) break;
+          ++unit;
+          tc_fence_after();
+          if (sn && elect_one()) {
 #pragma unroll
             for (int c = 0; c < 3; ++c) {
               const uint64_t b = dR + ((((kb + c) & (kRing - 1)) * kBox) >> 4);
@@ -349,14 +370,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_commit(empty(kb + 1));
             mma_commit(empty(kb + 2));
           }
-          mbar_arrive(turn(t ^ 1));
+          __syncwarp();
+          if (!sn && lane < 3) mbar_arrive(empty(kb + lane));
         }
-        __syncwarp();
-        if (pv) more = 1;
-        // boxes that this query tile has no use for
-        if (i >= 0 && !pv && lane < 2) mbar_arrive(empty(vb + lane));
-        if (i + 1 < x.n && !sn && lane < 3) mbar_arrive(empty(kb + lane));
+        if (both && lane == 0) mbar_arrive(turn(t ^ 1));
         box = kb + (i + 1 < x.n ? 3 : 0);
+        if (i < 0) nx = item_of(P, it);
       }
     }
     mma_commit_warp(drain);
@@ -364,43 +383,54 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------------------ softmax
-    const int t = (warp - 4) >> 2;
+    // Two warpgroups per query tile, each 64 of a key tile's columns (and of
+    // O's); a row's two threads share its reference, and meet at a barrier of
+    // their two warps.
+    const int t = ((warp - 4) >> 2) & 1, half = (warp - 4) >> 3;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t sc = tmem + lane_base + 128u * t;          // scores, then P
-    const uint32_t oc = tmem + lane_base + kColO + 128u * t;
+    const uint32_t oc = tmem + lane_base + kColO + 128u * t + 64u * half;
+    const uint32_t pair = 1 + 4 * t + (warp & 3);             // barrier of the row's two warps
+    float* xch = reinterpret_cast<float*>(smem + kOffXchg) + 128 * t + r;
     uint32_t ns = 0, no = 0;
     bool ok = true;
+    Item nx = item_of(P, blockIdx.x);
 #pragma unroll 1
-    for (int64_t it = blockIdx.x; ok && it < P.items; it += gridDim.x) {
-      const Item x = item_of(P, it);
-      if (t >= x.tiles) continue;
+    for (int it = blockIdx.x; ok && it < P.items;) {
+      const Item x = nx;
+      it += gridDim.x;
+      if (t >= x.tiles) {
+        nx = item_of(P, it);
+        continue;
+      }
       const Rows rr(P, x, t);
       const bool row_ok = t * kBM + r < x.rows;
       const int i = x.q0 + (row_ok ? t * kBM + r : x.rows - 1);   // local query index
       const int p = x.off + i;
       const int first = P.window > 0 ? max(0, p - P.window + 1) : 0;
-      float m = -INFINITY;
+      float m = 0.f;              // the row's reference
       float2 l = make_float2(0.f, 0.f);
 #pragma unroll 1
       for (int k = 0; k < x.n; ++k) {
         const int j = x.key_tile(k);
         if (!rr.any(P, j)) continue;
-        ok = all_wait(s_full(t), ns & 1, P.err);
-        if (!ok) break;
+        bool bad = !all_wait(s_full(t), ns & 1, P.err);
         ++ns;
         tc_fence_after();
-        uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
+        uint32_t see[2] = {~0u, ~0u};
         const bool whole = rr.all(P, j);
         if (!whole) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int s0 = j * kBN + 32 * c;
+          for (int c = 0; c < 2; ++c) {
+            const int s0 = j * kBN + 64 * half + 32 * c;
             see[c] = bit_range(first - s0, p + 1 - s0) | bit_range(0, min(P.sinks, p + 1) - s0);
           }
         }
+        uint32_t pk[32];
+        float2 sum;
         auto load = [&](int c, uint32_t (&v)[32]) {
-          tmem_ld_32x32b_x32(sc + 32u * c, v);
+          tmem_ld_32x32b_x32(sc + 64u * half + 32u * c, v);
           tmem_wait_ld();
           if (!whole) {
 #pragma unroll
@@ -408,52 +438,67 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!((see[c] >> e) & 1u)) v[e] = 0xff800000u;
           }
         };
-        uint32_t pk[64];
-        float2 sum;
-        float top;
-        // the weights over the reference m, and the largest exponent among them
+        // the weights over the reference m
         auto weigh = [&]() {
-          const float nm = m == -INFINITY ? 0.f : -m;
-          const float2 s2 = make_float2(P.scale_log2, P.scale_log2), n2 = make_float2(nm, nm);
-          top = -INFINITY;
+          const float2 s2 = make_float2(P.scale_log2, P.scale_log2), n2 = make_float2(-m, -m);
           sum = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < 2; ++c) {
             uint32_t v[32];
             load(c, v);
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const float2 y = __ffma2_rn(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])),
                                           s2, n2);
-              top = max3(top, y.x, y.y);
               const float2 w = make_float2(fast_exp2(y.x), fast_exp2(y.y));
               sum = __fadd2_rn(sum, w);
               pk[16 * c + e] = pack_bf16x2(w.x, w.y);
             }
           }
         };
-        bool again = m == -INFINITY;
-        if (!__all_sync(0xffffffffu, again)) {
+        bool again = false;
+        if (!bad) {
           weigh();
-          again = again || top > kSlack;
+          const float all = sum.x + sum.y;
+          again = all > kMost || (all < kLeast && l.x + l.y == 0.f && (see[0] | see[1]) != 0u);
         }
-        if (__any_sync(0xffffffffu, again)) {
+        // Both warps have read their scores (which P will overwrite), and agree
+        // on whether the references stand; the second vote takes them out
+        // together when a wait of one of them gave up.
+        if (named_bar_or(pair, 64, bad || again)) {
+          if (named_bar_or(pair, 64, bad)) {
+            ok = false;
+            break;
+          }
           // the tile's maximum first
           float mx = -INFINITY;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < 2; ++c) {
             uint32_t v[32];
-            tmem_ld_32x32b_x32(sc + 32u * c, v);
+            tmem_ld_32x32b_x32(sc + 64u * half + 32u * c, v);
             tmem_wait_ld();
-            const uint32_t bits = c == 0 ? see[0] : c == 1 ? see[1] : c == 2 ? see[2] : see[3];
+            const uint32_t bits = c == 0 ? see[0] : see[1];
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if ((bits >> e) & 1u) mx = fmaxf(mx, __uint_as_float(v[e]));
           }
           mx *= P.scale_log2;
+          // the row's maximum, and whether it has no weight yet, from both halves
+          if (half) *xch = mx;
+          named_bar_sync(pair, 64);
+          if (!half) *xch = mx = fmaxf(mx, *xch);
+          named_bar_sync(pair, 64);
+          if (half) mx = *xch;
+          named_bar_sync(pair, 64);
+          if (half) *xch = l.x + l.y;
+          named_bar_sync(pair, 64);
+          if (!half) *xch = l.x + l.y + *xch;
+          named_bar_sync(pair, 64);
+          const bool fresh = *xch == 0.f;
+          // up, or for a row without a weight yet also down
           float al = 1.f;
-          if (mx > m) {
-            al = fast_exp2(m - mx);                   // 0 when m = -inf
+          if (mx > m || (fresh && mx > -INFINITY)) {
+            al = fresh ? 0.f : fast_exp2(m - mx);
             m = mx;
             l = __fmul2_rn(l, make_float2(al, al));
           }
@@ -461,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // these scores'
           if (k > 0 && __any_sync(0xffffffffu, al != 1.f)) {
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < 2; ++c) {
               uint32_t o[32];
               tmem_ld_32x32b_x32(oc + 32u * c, o);
               tmem_wait_ld();
@@ -471,15 +516,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           weigh();
+          named_bar_sync(pair, 64);                   // the scores are read: P may overwrite them
         }
         l = __fadd2_rn(l, sum);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t w[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) w[e] = pk[32 * c + e];
-          tmem_st_32x32b_x32(sc + 32u * c, w);
-        }
+        tmem_st_32x32b_x32(sc + 32u * half, pk);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -487,32 +527,58 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // ---------------------------------------------------------- read-out
-      ok = all_wait(o_full(t), no & 1, P.err);
-      if (!ok) break;
+      const int64_t row = static_cast<int64_t>(x.cq + i) * P.H + x.h;
+      nx = item_of(P, it);        // (under the last product)
+      const bool bad = !all_wait(o_full(t), no & 1, P.err);
       ++no;
       tc_fence_after();
-      const float total = l.x + l.y;
+      float total = l.x + l.y;
+      if (half) *xch = total;
+      if (named_bar_or(pair, 64, bad)) {
+        ok = false;
+        break;
+      }
+      if (!half) *xch = total = total + *xch;
+      named_bar_sync(pair, 64);
+      if (half) total = *xch;
       const float inv = total == 0.f ? 0.f : 1.f / total;
-      const int64_t row = static_cast<int64_t>(x.cq + i) * P.H + x.h;
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
+      // Eight lanes trade their rows' 16-byte pieces, so that a store covers whole
+      // lines (a row's neighbour lies H * 256 bytes away: with a lane per row every
+      // store touched 32 lines, 4500 cycles for the tile).
+      uint32_t u[8][4];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
         uint32_t o[32];
         tmem_ld_32x32b_x32(oc + 32u * c, o);
         tmem_wait_ld();
-        if (row_ok) {
-          uint4* dst = reinterpret_cast<uint4*>(P.out + row * kDv + 32 * c);
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint4 w;
-            w.x = pack_bf16x2(__uint_as_float(o[e + 0]) * inv, __uint_as_float(o[e + 1]) * inv);
-            w.y = pack_bf16x2(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-            w.z = pack_bf16x2(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-            w.w = pack_bf16x2(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-            dst[e / 8] = w;
+        for (int e = 0; e < 16; ++e)
+          u[4 * c + e / 4][e & 3] =
+              pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+      }
+#pragma unroll
+      for (int d = 4; d > 0; d >>= 1) {
+        const bool up = (lane & d) != 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (j & d) continue;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? u[j][e] : u[j | d][e], d);
+            if (up) u[j][e] = got; else u[j | d][e] = got;
           }
         }
       }
-      if (row_ok && P.lse)
+      // u[j]: piece lane % 8 of row j of the eight
+      const int r0 = t * kBM + (warp & 3) * 32 + (lane & ~7);
+      __nv_bfloat16* dst = P.out + (static_cast<int64_t>(x.cq + x.q0 + r0) * P.H + x.h) * kDv +
+                           64 * half + 8 * (lane & 7);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (r0 + j < x.rows)
+          *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(j) * P.H * kDv) =
+              make_uint4(u[j][0], u[j][1], u[j][2], u[j][3]);
+      if (row_ok && half == 0 && P.lse)
         P.lse[row] = total == 0.f ? -INFINITY : (m + log2f(total)) * 0.69314718055994531f;
       // the next item's first product over O waits for this warp's P, which
       // comes after these reads
@@ -541,7 +607,7 @@ cudaError_t launch_window_mha(const CUtensorMap& tq, const CUtensorMap& tk, cons
   P.pairs = (a.max_len_q + 2 * kBM - 1) / (2 * kBM);
   P.window = a.window;
   P.sinks = a.sinks;
-  P.items = static_cast<int64_t>(a.B) * a.H * P.pairs;
+  P.items = a.B * a.H * P.pairs;     // (below 2^30: the caller checks)
   P.scale_log2 = a.sm_scale * 1.4426950408889634f;
   P.out = reinterpret_cast<__nv_bfloat16*>(a.out);
   P.lse = a.lse;

@@ -98,6 +98,19 @@ def test_references_left_behind(ramp):
         check(q, k, v, cu_q, cu_k, out, lse, window, sinks)
 
 
+@pytest.mark.parametrize("shift", [-300.0, -60.0, 60.0, 300.0])
+def test_scores_far_from_zero(shift):
+    """All of a row's scores far below or above zero, some rows changing sides."""
+    q, k, v, cu_q, cu_k, lens_q = make([400], None, 2, seed=87, q_mul=1.0)
+    q[:, :, 0] = 32.0
+    k[:, :, 0] = shift / (32.0 * SCALE)
+    k[200:260, :, 0] *= -1
+    for window, sinks in ((0, 0), (70, 2)):
+        out, lse = call(q, k, v, cu_q, cu_k, lens_q, [400], window, sinks)
+        assert_no_device_error()
+        check(q, k, v, cu_q, cu_k, out, lse, window, sinks)
+
+
 def test_another_sequences_nan_stays_there():
     lens = [200, 130, 77]
     q, k, v, cu_q, cu_k, lens_q = make(lens, None, 2, seed=82)
