@@ -22,7 +22,7 @@
 //  warps 1, 2  MMA issuers, one per query tile: S = Q K^T (12 MMAs, M128 N128
 //              K16), O += P V (8 MMAs, P read from TMEM, V MN-major from shared
 //              memory);
-//  warps 4..19 two warpgroups per query tile, a thread half a row: P over the
+//  warps 4..11 a warpgroup per query tile, a thread one row: P over the
 //              scores' own columns.  The running maximum of the tile before
 //              serves as the exponentials' reference; only where a row's weights
 //              over it add up to more than 2^32 is the tile's maximum taken
@@ -58,9 +58,8 @@ constexpr uint32_t kOffBar = kOffRing + kRing * kBox;
 // o_full[2], turn[2], drain
 constexpr uint32_t kNumBars = 4 + kRing + 12 + 1;
 constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;
-constexpr uint32_t kOffXchg = kOffMisc + 16;           // one float per row, between its two threads
-constexpr uint32_t kSmem = kOffXchg + 2 * 128 * 4 + 1024;
-constexpr int kThreads = 640;
+constexpr uint32_t kSmem = kOffMisc + 16 + 1024;
+constexpr int kThreads = 384;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;
 constexpr uint32_t kIdescS = instr_desc(kFmtBF16, kFmtBF16, 0, 0, kBM, kBN);
@@ -180,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(q_full(t), 1);
       mbar_init(q_empty(t), 1);
       mbar_init(s_full(t), 1);
-      mbar_init(p_full(t), 8);
+      mbar_init(p_full(t), 4);
       mbar_init(o_full(t), 1);
       mbar_init(turn(t), 1);
     }
@@ -383,16 +382,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------------------ softmax
-    // Two warpgroups per query tile, each 64 of a key tile's columns (and of
-    // O's); a row's two threads share its reference, and meet at a barrier of
-    // their two warps.
-    const int t = ((warp - 4) >> 2) & 1, half = (warp - 4) >> 3;
+    // A warpgroup per query tile, a thread one row.  (Two warpgroups a tile, half a
+    // row each, came out even: 1550 against 1700 cycles for the weights, and two
+    // barriers between the halves.)
+    const int t = (warp - 4) >> 2;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t sc = tmem + lane_base + 128u * t;          // scores, then P
-    const uint32_t oc = tmem + lane_base + kColO + 128u * t + 64u * half;
-    const uint32_t pair = 1 + 4 * t + (warp & 3);             // barrier of the row's two warps
-    float* xch = reinterpret_cast<float*>(smem + kOffXchg) + 128 * t + r;
+    const uint32_t oc = tmem + lane_base + kColO + 128u * t;
     uint32_t ns = 0, no = 0;
     bool ok = true;
     Item nx = item_of(P, blockIdx.x);
@@ -415,37 +412,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; k < x.n; ++k) {
         const int j = x.key_tile(k);
         if (!rr.any(P, j)) continue;
-        bool bad = !all_wait(s_full(t), ns & 1, P.err);
+        ok = all_wait(s_full(t), ns & 1, P.err);
+        if (!ok) break;
         ++ns;
         tc_fence_after();
-        uint32_t see[2] = {~0u, ~0u};
+        uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
         const bool whole = rr.all(P, j);
         if (!whole) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int s0 = j * kBN + 64 * half + 32 * c;
+          for (int c = 0; c < 4; ++c) {
+            const int s0 = j * kBN + 32 * c;
             see[c] = bit_range(first - s0, p + 1 - s0) | bit_range(0, min(P.sinks, p + 1) - s0);
           }
         }
-        uint32_t pk[32];
+        uint32_t pk[64];
         float2 sum;
-        auto load = [&](int c, uint32_t (&v)[32]) {
-          tmem_ld_32x32b_x32(sc + 64u * half + 32u * c, v);
-          tmem_wait_ld();
-          if (!whole) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!((see[c] >> e) & 1u)) v[e] = 0xff800000u;
-          }
-        };
-        // the weights over the reference m
+        // the weights over the reference m: 32 columns at a time, the next ones
+        // arriving under this one's arithmetic
         auto weigh = [&]() {
           const float2 s2 = make_float2(P.scale_log2, P.scale_log2), n2 = make_float2(-m, -m);
           sum = make_float2(0.f, 0.f);
+          auto part = [&](int c, uint32_t (&v)[32]) {
+            if (!whole) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t v[32];
-            load(c, v);
+              for (int e = 0; e < 32; ++e)
+                if (!((see[c] >> e) & 1u)) v[e] = 0xff800000u;
+            }
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const float2 y = __ffma2_rn(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])),
@@ -454,47 +446,39 @@ __global__ void __launch_bounds__(kThreads, 1)
               sum = __fadd2_rn(sum, w);
               pk[16 * c + e] = pack_bf16x2(w.x, w.y);
             }
-          }
+          };
+          uint32_t va[32], vb[32];
+          tmem_ld_32x32b_x32(sc, va);
+          tmem_wait_ld();
+          tmem_ld_32x32b_x32(sc + 32u, vb);
+          part(0, va);
+          tmem_wait_ld();
+          tmem_ld_32x32b_x32(sc + 64u, va);
+          part(1, vb);
+          tmem_wait_ld();
+          tmem_ld_32x32b_x32(sc + 96u, vb);
+          part(2, va);
+          tmem_wait_ld();
+          part(3, vb);
         };
-        bool again = false;
-        if (!bad) {
-          weigh();
-          const float all = sum.x + sum.y;
-          again = all > kMost || (all < kLeast && l.x + l.y == 0.f && (see[0] | see[1]) != 0u);
-        }
-        // Both warps have read their scores (which P will overwrite), and agree
-        // on whether the references stand; the second vote takes them out
-        // together when a wait of one of them gave up.
-        if (named_bar_or(pair, 64, bad || again)) {
-          if (named_bar_or(pair, 64, bad)) {
-            ok = false;
-            break;
-          }
+        weigh();
+        const float all = sum.x + sum.y;
+        const bool fresh = l.x + l.y == 0.f;          // the row has no weight yet
+        if (__any_sync(0xffffffffu, all > kMost || (all < kLeast && fresh &&
+                                                    (see[0] | see[1] | see[2] | see[3]) != 0u))) {
           // the tile's maximum first
           float mx = -INFINITY;
 #pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
+          for (int c = 0; c < 4; ++c) {
             uint32_t v[32];
-            tmem_ld_32x32b_x32(sc + 64u * half + 32u * c, v);
+            tmem_ld_32x32b_x32(sc + 32u * c, v);
             tmem_wait_ld();
-            const uint32_t bits = c == 0 ? see[0] : see[1];
+            const uint32_t bits = c == 0 ? see[0] : c == 1 ? see[1] : c == 2 ? see[2] : see[3];
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if ((bits >> e) & 1u) mx = fmaxf(mx, __uint_as_float(v[e]));
           }
           mx *= P.scale_log2;
-          // the row's maximum, and whether it has no weight yet, from both halves
-          if (half) *xch = mx;
-          named_bar_sync(pair, 64);
-          if (!half) *xch = mx = fmaxf(mx, *xch);
-          named_bar_sync(pair, 64);
-          if (half) mx = *xch;
-          named_bar_sync(pair, 64);
-          if (half) *xch = l.x + l.y;
-          named_bar_sync(pair, 64);
-          if (!half) *xch = l.x + l.y + *xch;
-          named_bar_sync(pair, 64);
-          const bool fresh = *xch == 0.f;
           // up, or for a row without a weight yet also down
           float al = 1.f;
           if (mx > m || (fresh && mx > -INFINITY)) {
@@ -506,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // these scores'
           if (k > 0 && __any_sync(0xffffffffu, al != 1.f)) {
 #pragma unroll 1
-            for (int c = 0; c < 2; ++c) {
+            for (int c = 0; c < 4; ++c) {
               uint32_t o[32];
               tmem_ld_32x32b_x32(oc + 32u * c, o);
               tmem_wait_ld();
@@ -516,10 +500,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           weigh();
-          named_bar_sync(pair, 64);                   // the scores are read: P may overwrite them
         }
         l = __fadd2_rn(l, sum);
-        tmem_st_32x32b_x32(sc + 32u * half, pk);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t w[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) w[e] = pk[32 * c + e];
+          tmem_st_32x32b_x32(sc + 32u * c, w);
+        }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -529,56 +518,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- read-out
       const int64_t row = static_cast<int64_t>(x.cq + i) * P.H + x.h;
       nx = item_of(P, it);        // (under the last product)
-      const bool bad = !all_wait(o_full(t), no & 1, P.err);
+      ok = all_wait(o_full(t), no & 1, P.err);
+      if (!ok) break;
       ++no;
       tc_fence_after();
-      float total = l.x + l.y;
-      if (half) *xch = total;
-      if (named_bar_or(pair, 64, bad)) {
-        ok = false;
-        break;
-      }
-      if (!half) *xch = total = total + *xch;
-      named_bar_sync(pair, 64);
-      if (half) total = *xch;
+      const float total = l.x + l.y;
       const float inv = total == 0.f ? 0.f : 1.f / total;
       // Eight lanes trade their rows' 16-byte pieces, so that a store covers whole
       // lines (a row's neighbour lies H * 256 bytes away: with a lane per row every
       // store touched 32 lines, 4500 cycles for the tile).
-      uint32_t u[8][4];
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        uint32_t u[8][4];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t o[32];
-        tmem_ld_32x32b_x32(oc + 32u * c, o);
-        tmem_wait_ld();
+        for (int c = 0; c < 2; ++c) {
+          uint32_t o[32];
+          tmem_ld_32x32b_x32(oc + 64u * half + 32u * c, o);
+          tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          u[4 * c + e / 4][e & 3] =
-              pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-      }
+          for (int e = 0; e < 16; ++e)
+            u[4 * c + e / 4][e & 3] =
+                pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+        }
 #pragma unroll
-      for (int d = 4; d > 0; d >>= 1) {
-        const bool up = (lane & d) != 0;
+        for (int d = 4; d > 0; d >>= 1) {
+          const bool up = (lane & d) != 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (j & d) continue;
+          for (int j = 0; j < 8; ++j) {
+            if (j & d) continue;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? u[j][e] : u[j | d][e], d);
-            if (up) u[j][e] = got; else u[j | d][e] = got;
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? u[j][e] : u[j | d][e], d);
+              if (up) u[j][e] = got; else u[j | d][e] = got;
+            }
           }
         }
-      }
-      // u[j]: piece lane % 8 of row j of the eight
-      const int r0 = t * kBM + (warp & 3) * 32 + (lane & ~7);
-      __nv_bfloat16* dst = P.out + (static_cast<int64_t>(x.cq + x.q0 + r0) * P.H + x.h) * kDv +
-                           64 * half + 8 * (lane & 7);
+        // u[j]: piece lane % 8 of row j of the eight
+        const int r0 = t * kBM + (warp & 3) * 32 + (lane & ~7);
+        __nv_bfloat16* dst = P.out + (static_cast<int64_t>(x.cq + x.q0 + r0) * P.H + x.h) * kDv +
+                             64 * half + 8 * (lane & 7);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (r0 + j < x.rows)
-          *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(j) * P.H * kDv) =
-              make_uint4(u[j][0], u[j][1], u[j][2], u[j][3]);
-      if (row_ok && half == 0 && P.lse)
+        for (int j = 0; j < 8; ++j)
+          if (r0 + j < x.rows)
+            *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(j) * P.H * kDv) =
+                make_uint4(u[j][0], u[j][1], u[j][2], u[j][3]);
+      }
+      if (row_ok && P.lse)
         P.lse[row] = total == 0.f ? -INFINITY : (m + log2f(total)) * 0.69314718055994531f;
       // the next item's first product over O waits for this warp's P, which
       // comes after these reads
