@@ -13,13 +13,15 @@
 //    32-bit keys in shared memory, read once.  Three histogram passes (11, 11
 //    and 10 bits from the top; the CTAs read one another's histograms through
 //    distributed shared memory) find the key T of the last entry kept and how
-//    many entries equal to it are kept.  Warps own contiguous stretches, so
-//    ballots and prefixes over warps and CTAs give every kept entry its slot in
+//    many entries equal to it are kept.  Lanes own contiguous stretches, so
+//    prefixes over lanes, warps and CTAs give every kept entry its slot in
 //    position order, ties to the lower position included.  A chain of
-//    barriers and shared-memory atomics bounds it, not the row's bytes: 13 us
-//    for rows of 131072, of which reading them at the memory's rate is 0.1 us.
+//    barriers and shared-memory atomics bounds it, not the row's bytes: 12 us
+//    for a row of 131072 (reading it 3.5, a histogram pass 2, the slots and the
+//    writes 3.5), of which its bytes at the memory's rate are 0.1 us.
 //  * move_kernel: a warp moves four latents at a time, nine 16-byte loads in
-//    flight per lane; bound by the memory (2304 bytes per kept entry).
+//    flight per lane; bound by the memory (2304 bytes per kept entry): 65536
+//    entries in about 30 us, 5 TB/s.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -39,7 +41,6 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kClusterC = 8;
 constexpr int kAhead = 16;                // loads in flight per thread while a row is read
-constexpr int kGo = 4;                   // keys per step of the passes over shared memory
 constexpr int kOneCta = 8192;            // rows of at most this many entries take one CTA
 
 struct Params {
@@ -69,13 +70,8 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
 }
 
-// Sum of the lanes below `upto` (v: one value per lane), the same in every lane.
-__device__ __forceinline__ uint32_t sum_below(uint32_t v, int upto) {
-  return __reduce_add_sync(0xffffffffu, static_cast<int>(threadIdx.x % 32) < upto ? v : 0u);
-}
-
 // Sum of the lanes below this one.
-__device__ __forceinline__ uint32_t sums_above(uint32_t v) {
+__device__ __forceinline__ uint32_t sum_before(uint32_t v) {
   uint32_t inc = v;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -85,14 +81,18 @@ __device__ __forceinline__ uint32_t sums_above(uint32_t v) {
   return inc - v;
 }
 
+// Where a warp's entry i lies in shared memory: a word of padding per 32, so
+// that lanes with stretches of their own do not meet in a bank.
+__device__ __forceinline__ int slot_of(int i) { return i + (i >> 5); }
+
 template <int C>
 __global__ void __launch_bounds__(kThreads, 1) select_kernel(const Params P) {
-  extern __shared__ uint32_t keys[];     // [kWarps * wseg]
-  __shared__ uint32_t hist[2][kBins];
-  __shared__ uint32_t wsum[kWarps], weq[kWarps];
-  __shared__ alignas(8) uint32_t groups[2][kBins / 32];   // by pass, as hist
-  __shared__ uint32_t found[2];          // the pass's bin, the rank left inside it
-  __shared__ alignas(8) uint32_t xch[2];            // this CTA's entries above T, equal to T
+  extern __shared__ uint32_t keys[];     // [kWarps][slot_of(wseg)]
+  __shared__ uint32_t hist[3][kBins];    // a buffer per pass: the other CTAs may still read the last
+  __shared__ alignas(8) uint32_t group[3][kBins / 32];
+  __shared__ uint32_t wgt[kWarps], weq[kWarps];
+  __shared__ uint32_t found[3];          // the pass's bin, the rank left inside it, whether that is all of it
+  __shared__ alignas(8) uint32_t xch[2]; // this CTA's entries above T, equal to T
   const int rank = C == 1 ? 0 : static_cast<int>(cg::this_cluster().block_rank());
   const int b = blockIdx.x / C;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -130,54 +130,41 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const Params P) {
   const int lo = P.sinks, m = n - P.sinks - P.recent;
   const int w0 = (rank * kWarps + warp) * P.wseg;
   const int len = min(max(m - w0, 0), P.wseg);
-  uint32_t* mine = keys + warp * P.wseg;
+  uint32_t* mine = keys + warp * slot_of(P.wseg);
   const float* src = row + lo + w0;
-  for (int i = tid; i < 2 * kBins; i += kThreads) (&hist[0][0])[i] = 0;
+  for (int i = tid; i < 3 * kBins; i += kThreads) (&hist[0][0])[i] = 0;
   __syncthreads();
-  // one warp's 32 keys into a histogram; lanes that agree (stretches of equal
-  // totals) count once
-  auto count = [&](uint32_t* h, bool in, uint32_t d) {
-    const uint32_t on = __ballot_sync(0xffffffffu, in);
-    if (on == 0) return;
-    const int lead = __ffs(on) - 1;
-    const uint32_t first = __shfl_sync(0xffffffffu, d, lead);
-    if (__all_sync(0xffffffffu, !in || d == first)) {
-      if (lane == lead) atomicAdd(h + d, static_cast<uint32_t>(__popc(on)));
-    } else if (in) {
-      atomicAdd(h + d, 1u);
-    }
-  };
   // the row is read once, and counted by its top 11 bits as it arrives
 #pragma unroll 1
-  for (int i = lane; i - lane < len; i += 32 * kAhead) {
+  for (int i = lane; i < len; i += 32 * kAhead) {
     float x[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) x[u] = i + 32 * u < len ? __ldg(src + i + 32 * u) : 0.f;
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const bool in = i + 32 * u < len;
-      const uint32_t k = order_key(x[u]);
-      if (in) mine[i + 32 * u] = k;
-      count(hist[0], in, k >> 21);
+      if (i + 32 * u < len) {
+        const uint32_t k = order_key(x[u]);
+        mine[slot_of(i + 32 * u)] = k;
+        atomicAdd(&hist[0][k >> 21], 1u);
+      }
     }
   }
 
-  uint32_t want = static_cast<uint32_t>(room), prefix = 0;
+  // keep every key above T and the first `want` equal ones
+  uint32_t want = static_cast<uint32_t>(room), prefix = 0, T = 0;
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const int up = pass == 1 ? 21 : 10;      // where the bits above the digit start
     const uint32_t mask = pass == 2 ? 1023u : 2047u;
-    uint32_t* h = hist[pass & 1];
-    uint32_t* group = groups[pass & 1];
-#pragma unroll 1
-    for (int i = lane; pass > 0 && i - lane < len; i += 32 * kGo) {
-      uint32_t k[kGo];
-#pragma unroll
-      for (int u = 0; u < kGo; ++u) k[u] = i + 32 * u < len ? mine[i + 32 * u] : 0u;
-#pragma unroll
-      for (int u = 0; u < kGo; ++u)
-        count(h, i + 32 * u < len && (k[u] >> up) == prefix, (k[u] >> shift) & mask);
+    uint32_t* h = hist[pass];
+    uint32_t* gr = group[pass];
+    if (pass > 0) {
+#pragma unroll 4
+      for (int i = lane; i < len; i += 32) {
+        const uint32_t k = mine[slot_of(i)];
+        if ((k >> up) == prefix) atomicAdd(h + ((k >> shift) & mask), 1u);
+      }
     }
     __syncthreads();
     // The bin of the want-th largest, in two steps from the top: the bins in 64
@@ -187,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const Params P) {
     {
       const uint32_t v0 = __reduce_add_sync(0xffffffffu, h[64 * warp + lane]);
       const uint32_t v1 = __reduce_add_sync(0xffffffffu, h[64 * warp + 32 + lane]);
-      if (lane == 0) *reinterpret_cast<uint2*>(group + 2 * warp) = make_uint2(v0, v1);
+      if (lane == 0) *reinterpret_cast<uint2*>(gr + 2 * warp) = make_uint2(v0, v1);
     }
     sync_all();
     if (warp == 0) {
@@ -195,59 +182,66 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const Params P) {
       uint32_t c0 = 0, c1 = 0;
 #pragma unroll
       for (int q = 0; q < C; ++q) {
-        const uint2 x = *reinterpret_cast<const uint2*>(remote(group, q) + 62 - 2 * lane);
+        const uint2 x = *reinterpret_cast<const uint2*>(remote(gr, q) + 62 - 2 * lane);
         c0 += x.y;
         c1 += x.x;
       }
-      uint32_t before = sums_above(c0 + c1);
+      uint32_t before = sum_before(c0 + c1);
       uint32_t g = 0, left = 0;
-      bool here = before < want && want <= before + c0 + c1;
+      const bool here = before < want && want <= before + c0 + c1;
       if (here) {
         const bool second = want > before + c0;
         g = 63 - 2 * lane - (second ? 1 : 0);
         left = want - before - (second ? c0 : 0);
       }
-      int who = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+      const int who = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
       g = __shfl_sync(0xffffffffu, g, who);
       left = __shfl_sync(0xffffffffu, left, who);
       // lane l: bin 32 g + 31 - l
       uint32_t c = 0;
 #pragma unroll
       for (int q = 0; q < C; ++q) c += remote(h, q)[32 * g + 31 - lane];
-      before = sums_above(c);
+      before = sum_before(c);
       if (before < left && left <= before + c) {
         found[0] = 32 * g + 31 - lane;
         found[1] = left - before;
+        found[2] = left - before == c ? 1u : 0u;      // every key of the bin is kept
       }
     }
     __syncthreads();
     prefix = (prefix << (pass == 2 ? 10 : 11)) | found[0];
     want = found[1];
-    // the next pass counts in the other buffer; no CTA reads this one's copy of
-    // it any more (all have passed this pass's barrier)
-    for (int i = tid; i < kBins; i += kThreads) hist[(pass & 1) ^ 1][i] = 0;
-    __syncthreads();
-  }
-  const uint32_t T = prefix;             // keep every key above T and the first `want` equal ones
-
-  uint32_t gt = 0, eq = 0;
-#pragma unroll 1
-  for (int i = lane; i - lane < len; i += 32 * kGo) {
-#pragma unroll
-    for (int u = 0; u < kGo; ++u) {
-      const bool ok = i + 32 * u < len;
-      const uint32_t k = ok ? mine[i + 32 * u] : 0u;
-      gt += __popc(__ballot_sync(0xffffffffu, ok && k > T));
-      eq += __popc(__ballot_sync(0xffffffffu, ok && k == T));
+    if (found[2] != 0u) {
+      // No need to look inside the bin: the cut lies below it.  (The usual end, after
+      // two passes of three.  The smallest key, -inf's, is 2^23 - 1: no bin starts at 0.)
+      T = (prefix << shift) - 1u;
+      want = 0;
+      break;
     }
+    T = prefix;
   }
-  if (lane == 0) {
-    wsum[warp] = gt;
-    weq[warp] = eq;
+
+  // Each lane owns a stretch of the warp's entries, so that slots follow from
+  // one prefix over lanes, warps and CTAs.
+  const int each = P.wseg / 32;
+  const int i0 = lane * each, i1 = min(i0 + each, len);
+  uint32_t above = 0, level = 0;         // its entries above T and equal to it (at most 32)
+#pragma unroll 4
+  for (int i = i0; i < i1; ++i) {
+    const uint32_t k = mine[slot_of(i)];
+    above |= (k > T ? 1u : 0u) << (i - i0);
+    level |= (k == T ? 1u : 0u) << (i - i0);
+  }
+  const uint32_t gt = __popc(above), eq = __popc(level);
+  uint32_t bg = sum_before(gt), be = sum_before(eq);
+  if (lane == 31) {
+    wgt[warp] = bg + gt;
+    weq[warp] = be + eq;
   }
   __syncthreads();
-  uint32_t bg = sum_below(wsum[lane], warp), be = sum_below(weq[lane], warp);
-  if (C > 1) {
+  bg += __reduce_add_sync(0xffffffffu, lane < warp ? wgt[lane] : 0u);
+  be += __reduce_add_sync(0xffffffffu, lane < warp ? weq[lane] : 0u);
+  if constexpr (C > 1) {
     if (tid == kThreads - 1) {
       xch[0] = bg + gt;
       xch[1] = be + eq;
@@ -261,33 +255,26 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const Params P) {
         be += o.y;
       }
     }
+    cg::this_cluster().barrier_arrive();
   }
-  const uint32_t lt = (1u << lane) - 1;
 #pragma unroll 1
-  for (int i = lane; i - lane < len; i += 32 * kGo) {
-    uint32_t k[kGo];
-#pragma unroll
-    for (int u = 0; u < kGo; ++u) k[u] = i + 32 * u < len ? mine[i + 32 * u] : 0u;
-#pragma unroll
-    for (int u = 0; u < kGo; ++u) {
-      const bool ok = i + 32 * u < len;
-      const uint32_t mg = __ballot_sync(0xffffffffu, ok && k[u] > T);
-      const uint32_t me = __ballot_sync(0xffffffffu, ok && k[u] == T);
-      const uint32_t g = bg + __popc(mg & lt), e = be + __popc(me & lt);
-      if (ok && (k[u] > T || (k[u] == T && e < want))) {
-        const int s = lo + w0 + i + 32 * u;
-        const int64_t j = P.sinks + static_cast<int64_t>(g) + min(e, want);
-        idx[j] = s;
-        // the total itself, from its key unless that stands for several
-        if (nm)
-          nm[j] = k[u] == 0xFFFFFFFFu || k[u] == 0x80000000u ? __ldg(row + s) : key_value(k[u]);
+  for (uint32_t left = above | level; left != 0; left &= left - 1) {
+    const int u = __ffs(left) - 1;
+    const bool over = (above >> u) & 1u;
+    if (over || be < want) {
+      const int s = lo + w0 + i0 + u;
+      const int64_t j = P.sinks + static_cast<int64_t>(bg) + min(be, want);
+      idx[j] = s;
+      // the total itself, from its key unless that stands for several
+      if (nm) {
+        const uint32_t k = mine[slot_of(i0 + u)];
+        nm[j] = k == 0xFFFFFFFFu || k == 0x80000000u ? __ldg(row + s) : key_value(k);
       }
-      bg += __popc(mg);
-      be += __popc(me);
     }
+    if (over) ++bg; else ++be;
   }
   // nobody's shared memory goes away while another CTA may still read it
-  if (C > 1) cg::this_cluster().sync();
+  if constexpr (C > 1) cg::this_cluster().barrier_wait();
 }
 
 // Four kept latents per warp: 288 pieces of 16 bytes, nine per lane.
@@ -372,7 +359,9 @@ cudaError_t launch_cache_evict(const CacheEvictArgs& a, DevErr err, cudaStream_t
   const int C = P.c.cap <= kOneCta ? 1 : kClusterC;
   const int warps = C * kWarps;
   P.wseg = ((P.c.cap + warps - 1) / warps + 31) / 32 * 32;
-  const size_t smem = static_cast<size_t>(kWarps) * P.wseg * 4;
+  static_assert(262144 / (kClusterC * kWarps) <= 1024 && kOneCta / kWarps <= 1024,
+                "at most 32 entries per lane");
+  const size_t smem = static_cast<size_t>(kWarps) * (P.wseg + P.wseg / 32) * 4;
   cudaError_t e = C == 1 ? launch_select<1>(P, smem, s) : launch_select<kClusterC>(P, smem, s);
   if (e != cudaSuccess) return e;
   const int most_kept = a.budget < P.c.cap ? a.budget : P.c.cap;
