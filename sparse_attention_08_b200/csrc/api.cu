@@ -747,7 +747,7 @@ dsa_status_t check_cache(const void* kv_cache, int64_t n_pages, int page_size,
 dsa::paged::Cache cache_of(const void* kv_cache, int64_t n_pages, int page_size,
                            int64_t page_stride, const int32_t* block_table, int64_t block_table_ld,
                            int max_pages, const int32_t* seq_lens, int B,
-                           int max_len_k, int window, int sinks) {
+                           int max_len_k, int window, int sinks, int max_box) {
   dsa::paged::Cache c;
   c.pool = static_cast<const uint8_t*>(kv_cache);
   c.page_stride = page_stride;
@@ -758,7 +758,7 @@ dsa::paged::Cache cache_of(const void* kv_cache, int64_t n_pages, int page_size,
   c.page = page_size;
   c.page_inv = ((uint64_t(1) << 43) + page_size - 1) / page_size;
   const int low = page_size & -page_size;
-  c.box = low < 128 ? low : 128;
+  c.box = low < max_box ? low : max_box;
   c.n_pages = static_cast<int>(n_pages);
   const int64_t held = static_cast<int64_t>(max_pages) * page_size;
   c.cap = held < max_len_k ? static_cast<int>(held) : max_len_k;
@@ -796,7 +796,7 @@ dsa_status_t dsa_paged_mla_decode(const void* q, const void* kv_cache, int64_t n
   if ((st = device_info(&dev)) != DSA_OK) return st;
   dsa::PagedDecodeArgs a;
   a.cache = cache_of(kv_cache, n_pages, page_size, page_stride, block_table, block_table_ld,
-                     max_pages, seq_lens, B, max_len_k, window, sinks);
+                     max_pages, seq_lens, B, max_len_k, window, sinks, 64);
   a.H = H;
   a.max_len_k = max_len_k;
   a.sm_scale = sm_scale;
@@ -834,7 +834,7 @@ dsa_status_t dsa_paged_attn_mass(const void* q, const void* kv_cache, int64_t n_
   if ((st = device_info(&dev)) != DSA_OK) return st;
   dsa::PagedMassArgs a;
   a.cache = cache_of(kv_cache, n_pages, page_size, page_stride, block_table, block_table_ld,
-                     max_pages, seq_lens, B, max_len_k, window, sinks);
+                     max_pages, seq_lens, B, max_len_k, window, sinks, 128);
   a.H = H;
   a.max_len_k = max_len_k;
   a.sm_scale = sm_scale;
@@ -887,7 +887,7 @@ dsa_status_t dsa_cache_evict(void* kv_cache, int64_t n_pages, int page_size, int
   if ((st = device_info(&dev)) != DSA_OK) return st;
   dsa::CacheEvictArgs a;
   a.cache = cache_of(kv_cache, n_pages, page_size, page_stride, block_table, block_table_ld,
-                     max_pages, seq_lens, B, max_len_k, 0, 0);
+                     max_pages, seq_lens, B, max_len_k, 0, 0, 128);
   a.mass = mass;
   a.ld_mass = ld_mass;
   a.budget = budget;

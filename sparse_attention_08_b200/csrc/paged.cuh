@@ -5,7 +5,7 @@
 // A cache is a pool of pages of `page` latent rows; row s of sequence b is row
 // s % page of pool page table[b, s / page].  The newest token of a sequence of
 // n entries sees all of them, or (window > 0) the entries s >= n - window and
-// s < sinks.  Keys are worked on in tiles of 128 positions; the tiles that
+// s < sinks.  Keys are worked on in tiles of kTile positions; the tiles that
 // hold a seen key are numbered 0 .. n_tiles-1 within the sequence.
 #pragma once
 
@@ -14,9 +14,7 @@
 namespace dsa {
 namespace paged {
 
-constexpr int kTile = 128;                      // keys per tile
 constexpr int kChunks = 9;                      // 64-column chunks of a 576-d row
-constexpr uint32_t kChunkBytes = kTile * 128;   // one chunk of a tile: 16 KB
 
 struct Cache {
   const int32_t* table;    // [B, table_ld]
@@ -27,7 +25,7 @@ struct Cache {
   int B;
   int page;                // rows per page, a multiple of 16
   uint64_t page_inv;       // 2^43 / page, rounded up: s / page = (s * page_inv) >> 43 for s < 2^24
-  int box;                 // rows per TMA box: the largest power of two <= 128 that divides page
+  int box;                 // rows per TMA box: a power of two that divides page, at most a tile
   int n_pages;             // pages in the pool
   int cap;                 // longest sequence the call allows
   int window, sinks;
@@ -45,6 +43,7 @@ __device__ __forceinline__ int seq_len(const Cache& c, int b) {
 
 // The tiles of a sequence that hold a seen key: the first `a` tiles (the
 // first tokens), then tiles from `w0` on (the window).
+template <int kTile>
 struct Seen {
   int len, lo, ns;   // seen: s < ns or lo <= s < len
   int a, w0, n;
@@ -56,8 +55,9 @@ struct Seen {
   }
 };
 
-__device__ __forceinline__ Seen seen_of(const Cache& c, int len) {
-  Seen k;
+template <int kTile>
+__device__ __forceinline__ Seen<kTile> seen_of(const Cache& c, int len) {
+  Seen<kTile> k;
   k.len = len;
   k.lo = c.window > 0 ? max(0, len - c.window) : 0;
   k.ns = min(c.sinks, k.lo);
@@ -120,6 +120,7 @@ struct Start {
 // Called by every thread of the CTA (nwarps whole warps); scratch: nwarps + 3 ints.
 // Warp w adds up sequences [w, w+1) * B / nwarps; the warp whose stretch holds
 // the piece's first tile then finds its sequence with a scan.
+template <int kTile>
 __device__ __forceinline__ Start find_start(const Cache& c, int range, int ranges, int min_tiles,
                                             int nwarps, int* scratch, const DevErr& err) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -131,7 +132,7 @@ __device__ __forceinline__ Start find_start(const Cache& c, int range, int range
   for (int b = b0 + lane; b < b1; b += 32) {
     const int raw = __ldg(c.lens + b);
     bad |= raw < 0 || raw > c.cap;
-    sum += max(seen_of(c, seq_len(c, b)).n, min_tiles);
+    sum += max(seen_of<kTile>(c, seq_len(c, b)).n, min_tiles);
   }
   if (bad && range == 0) raise_error(err, kErrBounds);
   sum = warp_sum(sum);
@@ -149,7 +150,7 @@ __device__ __forceinline__ Start find_start(const Cache& c, int range, int range
   if (first < total && first >= before && first < before + sum) {
 #pragma unroll 1
     for (int b = b0; b < b1; b += 32) {
-      const int n = b + lane < b1 ? max(seen_of(c, seq_len(c, b + lane)).n, min_tiles) : 0;
+      const int n = b + lane < b1 ? max(seen_of<kTile>(c, seq_len(c, b + lane)).n, min_tiles) : 0;
       int inc = n;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -175,10 +176,11 @@ __device__ __forceinline__ Start find_start(const Cache& c, int range, int range
 
 // Walks the tiles of one piece, segment by segment (a segment: the piece's
 // share of one sequence).  Every role of a CTA walks the same way.
+template <int kTile>
 struct Walk {
   const Cache& c;
   int b, i0, i1, left, min_tiles;
-  Seen k;
+  Seen<kTile> k;
   __device__ __forceinline__ Walk(const Cache& cache, const Start& s, int min_t)
       : c(cache), b(s.b), i0(s.skip), i1(0), left(s.per), min_tiles(min_t) {}
   // Moves to the next segment: sequence b, its tiles [i0, i1).
@@ -189,7 +191,7 @@ struct Walk {
     }
 #pragma unroll 1
     for (; left > 0 && b < c.B; ++b) {
-      k = seen_of(c, seq_len(c, b));
+      k = seen_of<kTile>(c, seq_len(c, b));
       const int n = max(k.n, min_tiles);
       if (n > i0) {
         i1 = min(n, i0 + left);
@@ -212,7 +214,7 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, 
 }
 
 // What a lane of the loading warp brings in of one tile: box `lane` of the
-// tile's 128 / box boxes, if it holds a seen key.
+// tile's kTile / box boxes, if it holds a seen key.
 struct Box {
   bool on;
   int32_t page, row;
@@ -226,7 +228,8 @@ __device__ __forceinline__ void prefetch_box(const Cache& c, const Box& x) {
                      static_cast<uint32_t>(c.box) * 1152u);
 }
 
-__device__ __forceinline__ Box box_of(const Cache& c, const Seen& k, int b, int tile, int lane,
+template <int kTile>
+__device__ __forceinline__ Box box_of(const Cache& c, const Seen<kTile>& k, int b, int tile, int lane,
                                       const DevErr& err) {
   Box x;
   const int s = tile * kTile + lane * c.box;
@@ -241,6 +244,20 @@ __device__ __forceinline__ Box box_of(const Cache& c, const Seen& k, int b, int 
     if (x.page < 0 || x.page >= c.n_pages) raise_error(err, kErrBounds);
   }
   return x;
+}
+
+// 16 lanes x 256 bits, repeated 4 times along the columns (32 columns): with t
+// the thread in the warp, registers 4i, 4i+1 hold lane addr.lane + t/4, columns
+// 8i + 2(t%4) + {0,1}; registers 4i+2, 4i+3 lane addr.lane + t/4 + 8.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
 }
 
 // Sums (or maxima) of 16 columns over the lanes of a warp: lanes i and i + 16

@@ -7,31 +7,34 @@
 //   out[b,h,:] = sum_{s in V_b} softmax_s(scale q[b,h,:] . x[s]) x[s, 0:512]
 //   lse[b,h]   = log sum_{s in V_b} exp(scale q[b,h,:] . x[s])
 //
-// One CTA works on up to 64 heads and a run of 128-key tiles.  The products
-// are formed with the KEYS (and then the value dims) as the MMA's 128 rows and
-// the heads as its columns:
+// One CTA works on up to 64 heads and a run of 64-key tiles.  The products are
+// formed with the KEYS (and then the value dims) as the MMA's rows and the heads
+// as its columns:
 //
-//   S^T [128 keys x 64 heads]     = X [128 x 576] Q^T       36 MMAs, M128 N64 K16
-//   O^T [4 x 128 dims x 64 heads] += X[:, 0:512]^T P^T       32 MMAs, M128 N64 K16
+//   S^T [64 keys x 64 heads]      = X [64 x 576] Q^T         36 MMAs, M64 N64 K16
+//   O^T [4 x 128 dims x 64 heads] += X[:, 0:512]^T P^T       16 MMAs, M128 N64 K16
 //
-// With the heads as rows a 64-head CTA could only issue M = 64 MMAs, which take
-// as long as M = 128 ones, and twice the time of these.  The latents are read
-// from shared memory as they lie: rows of 64-column chunks are K-major for
-// S^T and, transposed, MN-major for O^T.  A thread then holds one key and the
-// heads' scores side by side, so P^T (a key's 64 heads in 128 bytes) is written
-// as whole 16-byte pieces of an MN-major operand, without a transpose.
+// With the heads as rows the second product would be M = 64 too, at twice the
+// time (an M = 64 MMA costs about what an M = 128 one does).  The latents are read
+// from shared memory as they lie: rows of 64-column chunks are K-major for S^T
+// and, transposed, MN-major for O^T; P^T (a key's 64 heads in 128 bytes) is
+// written as an MN-major operand.
 //
 // The softmax needs no maximum over the lanes on the common path: any
 // reference m[h] within 2^32 of the row's maximum serves (P is bf16 and O fp32,
-// both with an 8-bit exponent), so a tile only votes whether a score exceeds
-// its reference by more; then the columns' maxima are reduced over the lanes
-// and O^T and the sums are rescaled.
+// both with an 8-bit exponent), so a tile only votes whether a key's weights
+// over the references exceed that; then the columns' maxima are reduced and
+// O^T and the sums are rescaled.
 //
-// Shared memory: the heads' queries (72 KB) and one tile (nine 16 KB chunks
-// in five parts with their own full and empty barriers).  P^T overwrites the
-// RoPE chunk, which the values do not need.  A part is reloaded as soon as its product is
-// done, so the next tile streams in behind O^T's products; 148 CTAs at
-// different points of that cycle keep the memory busy.
+// Shared memory: the heads' queries (72 KB) and two tiles (72 KB each, nine
+// chunks in five parts with their own empty barriers).  P^T overwrites the RoPE
+// chunk of its tile, which the values do not need.  A part is reloaded as soon as
+// its product is done.  The two tiles are half a cycle apart: the softmax of one
+// and the reload of its latents run under the products of the other.  (One tile
+// of 128 keys, M = 128 for S^T, needs fewer MMA cycles (3300 against 3900 per 128
+// keys) but leaves the tensor cores idle through its softmax and reload: 5900
+// cycles per 128 keys.)  Two issuers, one for the S^T products and one for the
+// O^T products, so that neither waits behind the other.
 //
 // The sequences' tiles stand in one line that is cut into equal pieces, one
 // per CTA (times the head groups, which read the same keys at the same time, so
@@ -51,32 +54,37 @@ namespace {
 
 using namespace paged;
 
+constexpr int kTile = 64;                             // keys per tile
 constexpr int kHeads = 64;                            // heads per CTA (MMA N)
 constexpr int kDv = 512;
+constexpr uint32_t kChunkBytes = kTile * 128;         // one 64-column chunk of a tile: 8 KB
+constexpr uint32_t kTileBytes = kChunks * kChunkBytes;
 constexpr uint32_t kQChunk = kHeads * 128;            // 8 KB
-constexpr uint32_t kOffX = 0;                         // the tile
-constexpr uint32_t kOffP = kOffX + 8 * kChunkBytes;   // P^T over the RoPE chunk
-constexpr uint32_t kOffQ = kOffX + kChunks * kChunkBytes;
+constexpr uint32_t kOffX = 0;                         // two tiles
+constexpr uint32_t kOffP = 8 * kChunkBytes;           // in a tile: P^T over the RoPE chunk
+constexpr uint32_t kOffQ = kOffX + 2 * kTileBytes;
 constexpr uint32_t kOffBar = kOffQ + kChunks * kQChunk;
 constexpr int kParts = 5;                             // chunk pairs 0..3, the RoPE chunk
-// barriers: full[3] (parts 0 and 1, parts 2 and 3, part 4), empty[5], q_full, q_empty, s_full, p_full, o_full, o_empty, drain
-constexpr uint32_t kNumBars = 3 + kParts + 7;
-constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;         // TMEM slot, plan scratch
-constexpr uint32_t kOffRef = (kOffMisc + 128 + 127) / 128 * 128;   // -m[64], alpha[64]
-constexpr uint32_t kOffRed = kOffRef + 2 * kHeads * 4;        // [4][64]
-constexpr uint32_t kSmem = kOffRed + 4 * kHeads * 4 + 1024;
-constexpr int kLoaders = 3;                           // loading warps: warp i brings in parts i, i + 3
-constexpr int kSoft = 16;                             // softmax warps: four warpgroups
-constexpr int kWide = kHeads * 4 / kSoft;             // heads per softmax thread
-constexpr int kSoftThreads = 32 * kSoft;
-constexpr int kWarps = kLoaders + 1 + kSoft;
+// barriers: per tile slot full[3] (parts 0 and 1, parts 2 and 3, part 4), empty[5], s_full, p_full;
+// then q_full, q_empty, o_full, o_empty, refs, pv_done, drain
+constexpr uint32_t kSlotBars = 3 + kParts + 2;
+constexpr uint32_t kNumBars = 2 * kSlotBars + 7;
+constexpr int kLoaders = 2;                           // loading warps: warp i brings in parts i, i + 2, i + 4
+constexpr int kIssueS = kLoaders, kIssueO = kLoaders + 1;
+constexpr int kSoft = 16;                             // softmax warps: eight per tile slot
+constexpr int kSoftThreads = 32 * kSoft, kGroupThreads = kSoftThreads / 2;
+constexpr int kWarps = kLoaders + 2 + kSoft;
 constexpr int kThreads = 32 * kWarps;
+constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;         // TMEM slot, plan scratch
+constexpr uint32_t kOffRef = (kOffMisc + 16 + (kWarps + 4) * 4 + 127) / 128 * 128;   // -m[64], alpha[64]
+constexpr uint32_t kOffRed = kOffRef + 2 * kHeads * 4;        // [8][64]
+constexpr uint32_t kSmem = kOffRed + 8 * kHeads * 4 + 1024;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0;                         // + 64 * (dims / 128)
-constexpr uint32_t kColS = 256;
-constexpr uint32_t kIdescS = instr_desc(kFmtBF16, kFmtBF16, 0, 0, 128, kHeads);
+constexpr uint32_t kColS = 256;                       // lanes 0-15 of each 32 for slot 0, 16-31 for slot 1
+constexpr uint32_t kIdescS = instr_desc(kFmtBF16, kFmtBF16, 0, 0, kTile, kHeads);
 constexpr uint32_t kIdescO = instr_desc(kFmtBF16, kFmtBF16, 1, 1, 128, kHeads);
-constexpr float kMost = 4294967296.f;                 // 2^32: largest sum of a key's weights over the references
+constexpr float kMost = 4294967296.f;                 // 2^32: largest sum of weights over the references
 constexpr float kNoRef = -1e30f;                      // no score yet: any finite one is above
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -102,12 +110,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bar0 = sbase + kOffBar;
-  auto full = [&](int part) { return bar0 + 8u * (part / 2); };
-  auto empty = [&](int i) { return bar0 + 8u * (3 + i); };
-  const uint32_t q_full = bar0 + 8u * (3 + kParts);
-  const uint32_t q_empty = q_full + 8, s_full = q_full + 16, p_full = q_full + 24;
-  const uint32_t o_full = q_full + 32, o_empty = q_full + 40, drain = q_full + 48;
+  auto full = [&](uint32_t slot, int part) { return bar0 + 8u * (slot * kSlotBars + part / 2); };
+  auto empty = [&](uint32_t slot, int part) { return bar0 + 8u * (slot * kSlotBars + 3 + part); };
+  auto s_full = [&](uint32_t slot) { return bar0 + 8u * (slot * kSlotBars + 3 + kParts); };
+  auto p_full = [&](uint32_t slot) { return bar0 + 8u * (slot * kSlotBars + 4 + kParts); };
+  const uint32_t q_full = bar0 + 8u * (2 * kSlotBars), q_empty = q_full + 8;
+  const uint32_t o_full = q_full + 16, o_empty = q_full + 24;
+  const uint32_t refs = q_full + 32, pv_done = q_full + 40, drain = q_full + 48;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + kOffMisc);
+  volatile uint32_t* version = tmem_slot + 1;       // counts the changes of the references
   int* scratch = reinterpret_cast<int*>(smem + kOffMisc + 16);
   float* ref = reinterpret_cast<float*>(smem + kOffRef);
   float* alpha = ref + kHeads;
@@ -120,22 +131,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int heads = min(kHeads, P.H - g * kHeads);
 
   if (threadIdx.x == 0) {
-    mbar_init(full(0), 2);
-    mbar_init(full(2), 2);
-    mbar_init(full(4), 1);
-    for (int i = 0; i < kParts; ++i) mbar_init(empty(i), 1);
+    for (uint32_t u = 0; u < 2; ++u) {
+      mbar_init(full(u, 0), 2);
+      mbar_init(full(u, 2), 2);
+      mbar_init(full(u, 4), 1);
+      for (int i = 0; i < kParts; ++i) mbar_init(empty(u, i), 1);
+      mbar_init(s_full(u), 1);
+      mbar_init(p_full(u), kSoft / 2);
+    }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
-    mbar_init(s_full, 1);
-    mbar_init(p_full, kSoft);
     mbar_init(o_full, 1);
     mbar_init(o_empty, kSoft);
-    mbar_init(drain, 1);
+    mbar_init(refs, kSoft / 2);
+    mbar_init(pv_done, 1);
+    mbar_init(drain, 2);
+    *version = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tq);
     tma_prefetch_desc(&tx);
   }
-  if (warp == kLoaders) {
+  if (warp == kIssueS) {
     tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), kTmemCols);
     tmem_relinquish();
   }
@@ -146,19 +162,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       reinterpret_cast<uint4*>(smem + kOffQ)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   tc_fence_before();
-  const Start start = find_start(P.c, piece, P.pieces, 1, kWarps, scratch, P.err);
+  const Start start = find_start<kTile>(P.c, piece, P.pieces, 1, kWarps, scratch, P.err);
   tc_fence_after();
   const uint32_t tmem = uniform(*tmem_slot);
   grid_release();
   if (blockIdx.x == 0 && threadIdx.x == 0) P.plan[P.c.B] = start.per;
-  Walk w(P.c, start, 1);
+  Walk<kTile> w(P.c, start, 1);
 
   if (warp < kLoaders) {
     // ------------------------------------------------------------ loads
-    // Lane i brings in box i of each of the warp's parts of a tile.  One warp
-    // alone would take longer over a tile's waits and copies (about 300
-    // cycles a part) than the tile's products leave between their parts.
-    uint32_t n = 0;               // tiles so far
+    // Lane i brings in box i of each of the warp's parts of a tile.
+    uint32_t n = 0;               // tiles so far: tile n uses slot n % 2
     bool ok = true;
     int seg = 0, stop = 0;        // segments whose queries, parts of tile n that were asked for
 #pragma unroll 1
@@ -171,36 +185,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < kChunks; ++c)
           tma_load_2d(sbase + kOffQ + c * kQChunk, &tq, 64 * c, w.b * P.H + g * kHeads, q_full);
       }
-      Box x = box_of(P.c, w.k, w.b, w.k.tile(w.i0), lane, P.err);
+      // page ids and an L2 prefetch two tiles ahead of the loads
+      Box x = box_of(P.c, w.k, w.b, w.k.tile(w.i0), lane, P.err), nx;
+      nx.on = false;
+      if (w.i0 + 1 < w.i1) nx = box_of(P.c, w.k, w.b, w.k.tile(w.i0 + 1), lane, P.err);
+      if (warp == 1) prefetch_box(P.c, nx);
 #pragma unroll 1
       for (int i = w.i0; i < w.i1; ++i, ++n) {
-        Box nx;                   // the next tile's page ids, fetched a tile ahead
-        nx.on = false;
-        if (i + 1 < w.i1) {
-          nx = box_of(P.c, w.k, w.b, w.k.tile(i + 1), lane, P.err);
-          if (warp == kLoaders - 1) prefetch_box(P.c, nx);
+        Box nnx;
+        nnx.on = false;
+        if (i + 2 < w.i1) {
+          nnx = box_of(P.c, w.k, w.b, w.k.tile(i + 2), lane, P.err);
+          if (warp == 1) prefetch_box(P.c, nnx);
         }
-        const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, x.on));
-        const uint32_t dst = sbase + kOffX + static_cast<uint32_t>(lane * P.c.box) * 128;
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, x.on)) *
+                               static_cast<uint32_t>(P.c.box) * 128;
+        const uint32_t slot = n & 1;
+        const uint32_t dst = sbase + kOffX + slot * kTileBytes +
+                             static_cast<uint32_t>(lane * P.c.box) * 128;
 #pragma unroll 1
         for (int c = warp; c < kParts; c += kLoaders) {
-          ok = all_wait(empty(c), (n & 1) ^ 1, P.err);
+          ok = all_wait(empty(slot, c), ((n >> 1) & 1) ^ 1, P.err);
           if (!ok) {
             stop = c;
             break;
           }
           const uint32_t cols = c < 4 ? 2u : 1u;
-          if (lane == 0)
-            mbar_arrive_expect_tx(full(c), boxes * cols * static_cast<uint32_t>(P.c.box) * 128);
+          if (lane == 0) mbar_arrive_expect_tx(full(slot, c), bytes * cols);
           __syncwarp();
           if (x.on)
 #pragma unroll 1
             for (uint32_t u = 0; u < cols; ++u)
               tma_load_3d(dst + (2 * c + u) * kChunkBytes, &tx, 64 * (2 * c + u), x.row, x.page,
-                          full(c));
+                          full(slot, c));
         }
         if (!ok) break;
         x = nx;
+        nx = nnx;
       }
       if (!ok) {
         ++seg;
@@ -211,71 +232,95 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && lane == 0) {
       if (warp == 0 && seg > 0) mbar_wait_drain(q_full, (seg - 1) & 1, P.err);
 #pragma unroll 1
-      for (int c = warp; c < kParts; c += kLoaders) {
-        const uint32_t asked = n + (c < stop ? 1 : 0);
-        if (asked > 0) mbar_wait_drain(full(c), (asked - 1) & 1, P.err);
-      }
+      for (uint32_t u = 0; u < 2; ++u)
+#pragma unroll 1
+        for (int c = warp; c < kParts; c += kLoaders) {
+          // tiles asked for in slot u: those before n, and n itself up to part `stop`
+          const uint32_t asked = (n + 1 - u) / 2 + ((n & 1) == u && c < stop ? 1 : 0);
+          if (asked > 0) mbar_wait_drain(full(u, c), (asked - 1) & 1, P.err);
+        }
     }
     __syncwarp();
-  } else if (warp == kLoaders) {
-    // ------------------------------------------------------------ MMA
+  } else if (warp == kIssueS) {
+    // ------------------------------------------------------------ S^T products
     // The whole warp walks the tiles and one elected lane issues each run of
     // MMAs: every operand stays warp-uniform.  (Issued from a one-lane branch an
     // MMA took about 90 cycles to issue, twice its own time.)
-    const uint64_t dXk = smem_desc(sbase + kOffX, 16, 1024, kSwizzle128B);
+    const uint64_t dX = smem_desc(sbase + kOffX, 16, 1024, kSwizzle128B);
     const uint64_t dQ = smem_desc(sbase + kOffQ, 16, 1024, kSwizzle128B);
-    const uint64_t dXv = smem_desc(sbase + kOffX, kChunkBytes, 1024, kSwizzle128B);
-    const uint64_t dP = smem_desc(sbase + kOffP, kChunkBytes, 1024, kSwizzle128B);
     uint32_t n = 0;
     bool ok = true;
+#pragma unroll 1
     for (int seg = 0; ok && w.next(seg == 0); ++seg) {
       ok = all_wait(q_full, seg & 1, P.err);
 #pragma unroll 1
       for (int i = w.i0; ok && i < w.i1; ++i, ++n) {
-        const bool last = i + 1 == w.i1;
+        const uint32_t slot = uniform(n & 1), ph = (n >> 1) & 1;
+        const uint64_t a = dX + ((slot * kTileBytes) >> 4);
+        const uint32_t d = tmem + kColS + (slot << 20);           // lane offset 16 for slot 1
+        // (the slot's last scores have been read: its latents could only be
+        // replaced after the product that their weights went into)
 #pragma unroll
         for (int c = 0; c < 8; c += 4) {
-          ok = ok && all_wait(full(c / 2), n & 1, P.err);
+          ok = ok && all_wait(full(slot, c / 2), ph, P.err);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < 16; ++kk)
-              mma_f16(tmem + kColS, dXk + (((c + kk / 4) * kChunkBytes + (kk % 4) * 32) >> 4),
+              mma_f16(d, a + (((c + kk / 4) * kChunkBytes + (kk % 4) * 32) >> 4),
                       dQ + (((c + kk / 4) * kQChunk + (kk % 4) * 32) >> 4), kIdescS,
                       c + kk > 0 ? 1u : 0u);
           }
           __syncwarp();
         }
-        ok = ok && all_wait(full(4), n & 1, P.err);
+        ok = ok && all_wait(full(slot, 4), ph, P.err);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_f16(tmem + kColS, dXk + ((8 * kChunkBytes + kk * 32) >> 4),
-                    dQ + ((8 * kQChunk + kk * 32) >> 4), kIdescS, 1u);
-          mma_commit(s_full);
-          if (last) mma_commit(q_empty);
+            mma_f16(d, a + ((8 * kChunkBytes + kk * 32) >> 4), dQ + ((8 * kQChunk + kk * 32) >> 4),
+                    kIdescS, 1u);
+          mma_commit(s_full(slot));
+          if (i + 1 == w.i1) mma_commit(q_empty);
         }
         __syncwarp();
-        // the last segment's O^T must have been read out
-        if (ok && i == w.i0 && seg > 0) ok = all_wait(o_empty, (seg - 1) & 1, P.err);
-        ok = ok && all_wait(p_full, n & 1, P.err);
+      }
+    }
+    mma_commit_warp(drain);
+    if (lane == 0) mbar_wait_drain(drain, 0, P.err);
+    __syncwarp();
+  } else if (warp == kIssueO) {
+    // ------------------------------------------------------------ O^T products
+    const uint64_t dX = smem_desc(sbase + kOffX, kChunkBytes, 1024, kSwizzle128B);
+    const uint64_t dP = smem_desc(sbase + kOffX + kOffP, kChunkBytes, 1024, kSwizzle128B);
+    uint32_t n = 0;
+    bool ok = true;
+#pragma unroll 1
+    for (int seg = 0; ok && w.next(seg == 0); ++seg) {
+      // the last segment's O^T must have been read out
+      if (seg > 0) ok = all_wait(o_empty, (seg - 1) & 1, P.err);
+#pragma unroll 1
+      for (int i = w.i0; ok && i < w.i1; ++i, ++n) {
+        const uint32_t slot = uniform(n & 1);
+        ok = all_wait(p_full(slot), (n >> 1) & 1, P.err);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
+          const uint64_t a = dX + ((slot * kTileBytes) >> 4), b = dP + ((slot * kTileBytes) >> 4);
           const uint32_t more = i > w.i0 ? 1u : 0u;
-#pragma unroll 1
+#pragma unroll
           for (int mt = 0; mt < 4; ++mt) {
 #pragma unroll
             for (int kk = 0; kk < kTile / 16; ++kk)
-              mma_f16(tmem + kColO + 64u * mt, dXv + ((mt * 2 * kChunkBytes + kk * 2048) >> 4),
-                      dP + ((kk * 2048) >> 4), kIdescO, kk > 0 ? 1u : more);
-            mma_commit(empty(mt));
+              mma_f16(tmem + kColO + 64u * mt, a + ((mt * 2 * kChunkBytes + kk * 2048) >> 4),
+                      b + ((kk * 2048) >> 4), kIdescO, kk > 0 ? 1u : more);
+            mma_commit(empty(slot, mt));
           }
-          mma_commit(empty(4));
-          if (last) mma_commit(o_full);
+          mma_commit(empty(slot, 4));
+          mma_commit(pv_done);
+          if (i + 1 == w.i1) mma_commit(o_full);
         }
         __syncwarp();
       }
@@ -285,158 +330,193 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax
-    // Four warpgroups; a thread owns one key of the tile (TMEM lane) and 16 of
-    // the heads.  (Two warpgroups of 32 heads a thread took 1.5 times as long over
-    // a tile: too few warps to cover each other's latencies.)
-    const int wg = (warp - kLoaders - 1) >> 2;
+    // Eight warps per tile slot, two per TMEM sub-partition: a warp has 16 of
+    // the tile's keys and 32 of the heads, a thread two keys and eight heads
+    // (lane t: keys t/4 and t/4 + 8, heads 8i + 2(t%4) + {0,1}).
+    const int grp = (warp - kLoaders - 2) >> 3;       // the slot
+    const int half = ((warp - kLoaders - 2) >> 2) & 1;
     const int sp = warp & 3;                          // TMEM sub-partition
-    const int r = sp * 32 + lane;                     // key in the tile
-    const int tid = threadIdx.x - 32 * (kLoaders + 1);                 // 0..511
-    const uint32_t lane_base = static_cast<uint32_t>(sp * 32) << 16;
-    const int h0 = kWide * wg;
-    uint8_t* prow = smem + kOffP + r * 128;
+    const int tid = threadIdx.x - 32 * (kLoaders + 2);        // 0..511
+    const int gtid = tid & (kGroupThreads - 1);       // in the group
+    const int ra = sp * 16 + lane / 4, rb = ra + 8;   // keys in the tile
+    const int hq = 32 * half + 2 * (lane & 3);        // heads hq + 8i + {0,1}
+    const uint32_t scores = tmem + kColS + 32u * half + (static_cast<uint32_t>(sp * 32 + 16 * grp) << 16);
+    uint8_t* tile = smem + kOffX + grp * kTileBytes;
+    const float2 sc = make_float2(P.scale_log2, P.scale_log2);
+    const uint32_t gbar = 1 + grp;
     uint32_t n = 0;
     bool ok = true;
-    for (int seg = 0; ok && w.next(seg == 0); ++seg) {
-      float2 l[kWide / 2];               // sums of P
+#pragma unroll 1
+    for (int seg = 0; w.next(seg == 0); ++seg) {
+      float2 l[4], rr[4];         // sums of the weights, and the references they are over
+      uint32_t seen_version = 0;
+      bool mine = false;          // a tile of this segment was this group's
 #pragma unroll
-      for (int e = 0; e < kWide / 2; ++e) l[e] = make_float2(0.f, 0.f);
+      for (int e = 0; e < 4; ++e) l[e] = rr[e] = make_float2(0.f, 0.f);
 #pragma unroll 1
       for (int i = w.i0; i < w.i1; ++i, ++n) {
-        const bool seen = w.k.key(w.k.tile(i) * kTile + r);
-        const bool bad = !all_wait(s_full, n & 1, P.err);
-        const float2 sc = make_float2(P.scale_log2, P.scale_log2);
-        float2 y[kWide / 2];             // scores over the references, log2 units
+        if (static_cast<int>(n & 1) != grp || !ok) continue;
+        const int s0 = w.k.tile(i) * kTile;
+        const bool sa = w.k.key(s0 + ra), sb = w.k.key(s0 + rb);
+        // the tile before has settled the references
+        bool bad = n > 0 && !all_wait(refs, (n - 1) & 1, P.err);
+        bad = bad || !all_wait(s_full(grp), (n >> 1) & 1, P.err);
+        float2 ya[4], yb[4];      // scores, then over the references, then weights
         auto load = [&]() {
-          uint32_t v[kWide];
-          tmem_ld_x16(tmem + lane_base + kColS + h0, v);
+          uint32_t v[16];
+          tmem_ld_16x256b_x4(scores, v);
           tmem_wait_ld();
-          if (!seen)
 #pragma unroll
-            for (int e = 0; e < kWide; ++e) v[e] = 0xff800000u;
-#pragma unroll
-          for (int e = 0; e < kWide / 2; ++e)
-            y[e] = make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
-        };
-        auto shift = [&]() {
-#pragma unroll
-          for (int e = 0; e < kWide / 2; e += 2) {
-            const float4 m = *reinterpret_cast<const float4*>(ref + h0 + 2 * e);
-            y[e] = __ffma2_rn(y[e], sc, make_float2(m.x, m.y));
-            y[e + 1] = __ffma2_rn(y[e + 1], sc, make_float2(m.z, m.w));
+          for (int e = 0; e < 4; ++e) {
+            ya[e] = sa ? make_float2(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]))
+                       : make_float2(-INFINITY, -INFINITY);
+            yb[e] = sb ? make_float2(__uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]))
+                       : make_float2(-INFINITY, -INFINITY);
           }
+        };
+        // takes over the references in shared memory, and brings the sums to them
+        auto adopt = [&]() {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 m = *reinterpret_cast<const float2*>(ref + hq + 8 * e);
+            if (mine)
+              l[e] = __fmul2_rn(l[e], make_float2(fast_exp2(m.x - rr[e].x), fast_exp2(m.y - rr[e].y)));
+            rr[e] = m;
+          }
+          seen_version = *version;
+          mine = true;
+        };
+        auto weigh = [&]() -> float {
+          float2 all = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            ya[e] = __ffma2_rn(ya[e], sc, rr[e]);
+            yb[e] = __ffma2_rn(yb[e], sc, rr[e]);
+            ya[e] = make_float2(fast_exp2(ya[e].x), fast_exp2(ya[e].y));
+            yb[e] = make_float2(fast_exp2(yb[e].x), fast_exp2(yb[e].y));
+            all = __fadd2_rn(all, __fadd2_rn(ya[e], yb[e]));
+          }
+          return all.x + all.y;
         };
         bool over = false;
         if (!bad) {
           tc_fence_after();
           load();
-          if (i > w.i0) shift();
-        }
-        // the weights, in the hope that the references stand
-        uint32_t pk[kWide / 2];
-        auto weigh = [&]() {
-#pragma unroll
-          for (int e = 0; e < kWide / 2; ++e) {
-            y[e] = make_float2(fast_exp2(y[e].x), fast_exp2(y[e].y));
-            pk[e] = pack_bf16x2(y[e].x, y[e].y);
+          if (i > w.i0) {
+            if (!mine || *version != seen_version) adopt();
+            over = weigh() > kMost;           // (a weight above it makes the sum so)
           }
-        };
-        if (i > w.i0 && !bad) {
-          weigh();
-          float2 all = y[0];
-#pragma unroll
-          for (int e = 1; e < kWide / 2; ++e) all = __fadd2_rn(all, y[e]);
-          over = all.x + all.y > kMost;       // (a weight above it makes the sum so)
         }
-        // one vote for all the warps; it also takes them out together when
-        // a wait of one of them gave up
-        if (named_bar_or(1, kSoftThreads, bad || over) || i == w.i0) {
-          if (named_bar_or(1, kSoftThreads, bad)) {
+        // one vote for the group; it also takes its warps out together when a
+        // wait of one of them gave up
+        if (named_bar_or(gbar, kGroupThreads, bad || over) || i == w.i0) {
+          if (named_bar_or(gbar, kGroupThreads, bad)) {
             ok = false;
-            break;
+            continue;                         // (on to the segment's end, where all meet)
           }
           // new references: the columns' maxima over the tile
           if (i > w.i0) load();
-          float m[kWide];
 #pragma unroll
-          for (int e = 0; e < kWide / 2; ++e) {
-            m[2 * e] = y[e].x * P.scale_log2;
-            m[2 * e + 1] = y[e].y * P.scale_log2;
+          for (int e = 0; e < 4; ++e) {
+            float2 m = make_float2(fmaxf(ya[e].x, yb[e].x) * P.scale_log2,
+                                   fmaxf(ya[e].y, yb[e].y) * P.scale_log2);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) {
+              m.x = fmaxf(m.x, __shfl_xor_sync(0xffffffffu, m.x, d));
+              m.y = fmaxf(m.y, __shfl_xor_sync(0xffffffffu, m.y, d));
+            }
+            if (lane < 4) *reinterpret_cast<float2*>(red + sp * kHeads + hq + 8 * e) = m;
           }
-          const float top = column_reduce<true>(m);
-          if (lane < kWide) red[sp * kHeads + h0 + lane] = top;
-          named_bar_sync(1, kSoftThreads);
-          if (tid < kHeads) {
-            const float old = i > w.i0 ? -ref[tid] : kNoRef;
-            const float top = fmaxf(fmaxf(red[tid], red[kHeads + tid]),
-                                    fmaxf(red[2 * kHeads + tid], red[3 * kHeads + tid]));
+          named_bar_sync(gbar, kGroupThreads);
+          if (gtid < kHeads) {
+            const float old = i > w.i0 ? -ref[gtid] : kNoRef;
+            const float top = fmaxf(fmaxf(red[gtid], red[kHeads + gtid]),
+                                    fmaxf(red[2 * kHeads + gtid], red[3 * kHeads + gtid]));
             const float now = fmaxf(old, top);
-            alpha[tid] = fast_exp2(old - now);
-            ref[tid] = -now;
+            alpha[gtid] = fast_exp2(old - now);
+            ref[gtid] = -now;
+            if (gtid == 0) *version = *version + 1;
           }
-          named_bar_sync(1, kSoftThreads);
+          named_bar_sync(gbar, kGroupThreads);
           if (i > w.i0) {
-#pragma unroll
-            for (int e = 0; e < kWide / 2; ++e)
-              l[e] = __fmul2_rn(l[e], *reinterpret_cast<const float2*>(alpha + h0 + 2 * e));
-            // every earlier product is complete: this tile's last chunk could
-            // only be loaded after it
+            // O^T up to the tile before, in the new measure
+            bad = !all_wait(pv_done, (n - 1) & 1, P.err);
+            if (named_bar_or(gbar, kGroupThreads, bad)) {
+              ok = false;
+              continue;
+            }
+            tc_fence_after();
 #pragma unroll 1
-            for (int mt = 0; mt < 4; ++mt) {
-              uint32_t o[kWide];
-              tmem_ld_x16(tmem + lane_base + kColO + 64u * mt + h0, o);
+            for (int c = 8 * half; c < 8 * half + 8; ++c) {
+              uint32_t o[16];
+              const uint32_t at = tmem + kColO + 16u * c + (static_cast<uint32_t>(sp * 32) << 16);
+              tmem_ld_x16(at, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < kWide; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha[h0 + e]);
-              tmem_st_x16(tmem + lane_base + kColO + 64u * mt + h0, o);
+              for (int e = 0; e < 16; ++e)
+                o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha[(16 * c + e) & (kHeads - 1)]);
+              tmem_st_x16(at, o);
             }
             tmem_wait_st();
           }
-          shift();
+          adopt();
           weigh();
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(refs);
 #pragma unroll
-        for (int e = 0; e < kWide / 2; e += 4)
-          *reinterpret_cast<uint4*>(prow + ((h0 / 8 + e / 4) ^ (r & 7)) * 16) =
-              make_uint4(pk[e], pk[e + 1], pk[e + 2], pk[e + 3]);
+        for (int e = 0; e < 4; ++e) {
+          l[e] = __fadd2_rn(l[e], __fadd2_rn(ya[e], yb[e]));
+          const uint32_t at = ((4 * half + e) ^ (lane / 4)) * 16 + 4 * (lane & 3);
+          *reinterpret_cast<uint32_t*>(tile + kOffP + ra * 128 + at) = pack_bf16x2(ya[e].x, ya[e].y);
+          *reinterpret_cast<uint32_t*>(tile + kOffP + rb * 128 + at) = pack_bf16x2(yb[e].x, yb[e].y);
+        }
         // an unseen row of the tile holds whatever its memory held: its
         // weight is 0, and so must its value be (0 * NaN is not)
-        if (!seen) {
+        const int row = gtid >> 2;
+        if (!w.k.key(s0 + row)) {
 #pragma unroll 1
-          for (int c = 2 * wg; c < 2 * wg + 2; ++c)
+          for (int c = 2 * (gtid & 3); c < 2 * (gtid & 3) + 2; ++c)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<uint4*>(smem + kOffX + c * kChunkBytes + r * 128 + (j ^ (r & 7)) * 16) =
+              *reinterpret_cast<uint4*>(tile + c * kChunkBytes + row * 128 + (j ^ (row & 7)) * 16) =
                   make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full);
-#pragma unroll
-        for (int e = 0; e < kWide / 2; ++e) l[e] = __fadd2_rn(l[e], y[e]);
+        if (lane == 0) mbar_arrive(p_full(grp));
       }
-      if (!ok) break;
       // ---------------------------------------------------------- read-out
-      float ls[kWide];
-#pragma unroll
-      for (int e = 0; e < kWide / 2; ++e) {
-        ls[2 * e] = l[e].x;
-        ls[2 * e + 1] = l[e].y;
-      }
-      const float part = column_reduce<false>(ls);
-      if (lane < kWide) red[sp * kHeads + h0 + lane] = part;
-      const bool bad = !all_wait(o_full, seg & 1, P.err);
-      if (named_bar_or(1, kSoftThreads, bad)) {
+      // All sixteen warps: the sums of both groups, in the last references.
+      bool bad = !ok || !all_wait(o_full, seg & 1, P.err);
+      if (named_bar_or(3, kSoftThreads, bad)) {
         ok = false;
         break;
       }
       tc_fence_after();
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float2 t = l[e];
+        if (mine) {
+          const float2 m = *reinterpret_cast<const float2*>(ref + hq + 8 * e);
+          t = __fmul2_rn(t, make_float2(fast_exp2(m.x - rr[e].x), fast_exp2(m.y - rr[e].y)));
+        }
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+          t.x += __shfl_xor_sync(0xffffffffu, t.x, d);
+          t.y += __shfl_xor_sync(0xffffffffu, t.y, d);
+        }
+        if (lane < 4) *reinterpret_cast<float2*>(red + (4 * grp + sp) * kHeads + hq + 8 * e) = t;
+      }
+      named_bar_sync(3, kSoftThreads);
       const int tiles = max(w.k.n, 1);
       const bool whole = w.i0 == 0 && w.i1 == tiles;
       const int64_t slot = (static_cast<int64_t>(piece) * 2 + (seg == 0 ? 0 : 1)) * P.groups + g;
       if (tid < heads) {
-        const float sum = (red[tid] + red[kHeads + tid]) + (red[2 * kHeads + tid] + red[3 * kHeads + tid]);
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum += red[e * kHeads + tid];
         const int64_t at = static_cast<int64_t>(w.b) * P.H + g * kHeads + tid;
         if (whole) {
           if (P.lse) P.lse[at] = sum == 0.f ? -INFINITY : (log2f(sum) - ref[tid]) * kLn2;
@@ -447,11 +527,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (w.i0 == 0 && g == 0 && tid == 0)
         P.plan[w.b] = piece * start.per + start.per - w.left - (w.i1 - w.i0);
-      named_bar_sync(1, kSoftThreads);
+      named_bar_sync(3, kSoftThreads);
+      const int h0 = 16 * (tid >> 7);                 // a warp's 16 heads of O^T's 128 lanes
 #pragma unroll 1
       for (int mt = 0; mt < 4; ++mt) {
-        uint32_t o[kWide];
-        tmem_ld_x16(tmem + lane_base + kColO + 64u * mt + h0, o);
+        uint32_t o[16];
+        tmem_ld_x16(tmem + kColO + 64u * mt + h0 + (static_cast<uint32_t>(sp * 32) << 16), o);
         tmem_wait_ld();
         if (whole) {
           // lanes hold neighbouring dims: pairs of lanes swap so that each
@@ -459,19 +540,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int d = mt * 128 + sp * 32 + (lane & ~1);
           __nv_bfloat16* dst = P.out + (static_cast<int64_t>(w.b) * P.H + g * kHeads + h0) * kDv + d;
 #pragma unroll
-          for (int e = 0; e < kWide; e += 2) {
+          for (int e = 0; e < 16; e += 2) {
             const float2 iv = *reinterpret_cast<const float2*>(alpha + h0 + e);
             const float a = __uint_as_float(o[e]) * iv.x, b = __uint_as_float(o[e + 1]) * iv.y;
             const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? a : b, 1);
             const int h = e + (lane & 1);
             if (h0 + h < heads)
-              *reinterpret_cast<uint32_t*>(dst + static_cast<int64_t>(h) * kDv) =
+              *reinterpret_cast<uint32_t*>(dst + h * kDv) =
                   (lane & 1) ? pack_bf16x2(got, b) : pack_bf16x2(a, got);
           }
         } else {
-          float* dst = P.part + (slot * kHeads + h0) * kDv + mt * 128 + r;
+          float* dst = P.part + (slot * kHeads + h0) * kDv + mt * 128 + sp * 32 + lane;
 #pragma unroll
-          for (int e = 0; e < kWide; ++e)
+          for (int e = 0; e < 16; ++e)
             if (h0 + e < heads) dst[e * kDv] = __uint_as_float(o[e]);
         }
       }
@@ -479,13 +560,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(o_empty);
       // the references and sums are read above; the next segment rewrites them
-      named_bar_sync(1, kSoftThreads);
+      named_bar_sync(3, kSoftThreads);
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kLoaders) {
+  if (warp == kIssueS) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -506,7 +587,7 @@ __global__ void __launch_bounds__(128 * kJoin) combine_kernel(Params P) {
   grid_wait();
   const int per = P.plan[P.c.B];
   const int t0 = P.plan[b];
-  const int n = max(seen_of(P.c, seq_len(P.c, b)).n, 1);
+  const int n = max(seen_of<kTile>(P.c, seq_len(P.c, b)).n, 1);
   const int r0 = t0 / per, r1 = (t0 + n - 1) / per;
   if (r0 == r1) return;
   const int parts = r1 - r0 + 1;

@@ -33,6 +33,8 @@ namespace {
 
 using namespace paged;
 
+constexpr int kTile = 128;                             // keys per tile (MMA M)
+constexpr uint32_t kChunkBytes = kTile * 128;          // one 64-column chunk of a tile: 16 KB
 constexpr int kMaxStages = 12;
 constexpr uint32_t kOffBar = 0;                       // full[12], empty[12], q_full, q_empty, s_full[2], s_empty[2], drain
 constexpr uint32_t kNumBars = 2 * kMaxStages + 7;
@@ -100,10 +102,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  const Start start = find_start(P.c, blockIdx.x, P.pieces, 0, kWarps, scratch, P.err);
+  const Start start = find_start<kTile>(P.c, blockIdx.x, P.pieces, 0, kWarps, scratch, P.err);
   tc_fence_after();
   const uint32_t tmem = uniform(*tmem_slot);
-  Walk w(P.c, start, 0);
+  Walk<kTile> w(P.c, start, 0);
 
   if (warp < 2) {
     // ------------------------------------------------------------ loads
@@ -261,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (P.in != P.out) {
 #pragma unroll 1
       for (int b = 0; b < P.c.B; ++b) {
-        const Seen k = seen_of(P.c, seq_len(P.c, b));
+        const Seen<kTile> k = seen_of<kTile>(P.c, seq_len(P.c, b));
         const int64_t row = static_cast<int64_t>(b) * P.ld;
 #pragma unroll 1
         for (int s = k.a * kTile + blockIdx.x * 128 + tid; s < k.w0 * kTile; s += gridDim.x * 128)
