@@ -558,6 +558,7 @@ def dsa_window_mha_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, B, max_len_q, max_le
     (bf16) and lse [T_q, H] (fp32, optional)."""
     import torch
     bf16, i32 = torch.bfloat16, torch.int32
+    B = int(B)
     dev = _cuda(q, "q")
     pq = _ten(q, bf16, (None, None, None), dev, "q")
     T_q, H, d_qk = q.shape
@@ -570,8 +571,9 @@ def dsa_window_mha_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, B, max_len_q, max_le
     cq = _ten(cu_seqlens_q, i32, (B + 1,), dev, "cu_seqlens_q")
     ck = _ten(cu_seqlens_k, i32, (B + 1,), dev, "cu_seqlens_k")
     with _On(dev, stream) as st:
-        rc = load().dsa_window_mha_fwd(pq, pk, pv, cq, ck, B, max_len_q, max_len_k, T_q, T_k, H,
-                                       d_qk, d_v, window, sinks, sm_scale, po, pl, st)
+        rc = load().dsa_window_mha_fwd(pq, pk, pv, cq, ck, B, int(max_len_q), int(max_len_k), T_q,
+                                       T_k, H, d_qk, d_v, int(window), int(sinks),
+                                       float(sm_scale), po, pl, st)
     _check(rc, "dsa_window_mha_fwd")
 
 
@@ -589,6 +591,7 @@ def dsa_paged_mla_decode(q, kv_cache, block_table, seq_lens, max_len_k, sm_scale
     (uint8 CUDA tensor) is allocated here, on the call's stream, when not
     given."""
     import torch
+    max_len_k = int(max_len_k)
     cache, dev = _cache(kv_cache, block_table, seq_lens)
     B = cache[-1]
     pq = _ten(q, torch.bfloat16, (B, None, None), dev, "q")
@@ -602,8 +605,9 @@ def dsa_paged_mla_decode(q, kv_cache, block_table, seq_lens, max_len_k, sm_scale
             nbytes = lib.dsa_paged_mla_decode_workspace_size(B, H, max_len_k)
             workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
             pw = workspace.data_ptr()
-        rc = lib.dsa_paged_mla_decode(pq, *cache, max_len_k, H, d_qk, out.shape[2], window, sinks,
-                                      sm_scale, po, pl, pw, workspace.numel(), st)
+        rc = lib.dsa_paged_mla_decode(pq, *cache, max_len_k, H, d_qk, out.shape[2], int(window),
+                                      int(sinks), float(sm_scale), po, pl, pw, workspace.numel(),
+                                      st)
     _check(rc, "dsa_paged_mla_decode")
 
 
@@ -615,6 +619,7 @@ def dsa_paged_attn_mass(q, kv_cache, block_table, seq_lens, lse, max_len_k, sm_s
     arguments (see include/dsa.h)."""
     import torch
     f32 = torch.float32
+    max_len_k = int(max_len_k)
     cache, dev = _cache(kv_cache, block_table, seq_lens)
     B = cache[-1]
     pq = _ten(q, torch.bfloat16, (B, None, None), dev, "q")
@@ -625,8 +630,8 @@ def dsa_paged_attn_mass(q, kv_cache, block_table, seq_lens, lse, max_len_k, sm_s
     if pi is not None and ld_in != ld and B > 1:
         raise ValueError("mass_in and mass_out must have the same row stride")
     with _On(dev, stream) as st:
-        rc = load().dsa_paged_attn_mass(pq, *cache, max_len_k, H, d_qk, window, sinks, sm_scale,
-                                        pl, pi, po, ld, st)
+        rc = load().dsa_paged_attn_mass(pq, *cache, max_len_k, H, d_qk, int(window), int(sinks),
+                                        float(sm_scale), pl, pi, po, ld, st)
     _check(rc, "dsa_paged_attn_mass")
 
 
@@ -639,6 +644,7 @@ def dsa_cache_evict(kv_cache, block_table, seq_lens, mass, max_len_k, budget, si
     [B, >= budget] (optional).  See include/dsa.h."""
     import torch
     i32, f32 = torch.int32, torch.float32
+    max_len_k, budget = int(max_len_k), int(budget)
     cache, dev = _cache(kv_cache, block_table, seq_lens)
     B = cache[-1]
     pm, ld = _rows(mass, f32, B, max_len_k, dev, "mass")
@@ -647,8 +653,8 @@ def dsa_cache_evict(kv_cache, block_table, seq_lens, mass, max_len_k, budget, si
     pi = _ten(idx_out, i32, (B, budget), dev, "idx_out")
     po, ld_o = _rows(new_mass, f32, B, budget, dev, "new_mass")
     with _On(dev, stream) as st:
-        rc = load().dsa_cache_evict(*cache, max_len_k, pm, ld, budget, sinks, recent, pt, ld_t,
-                                    new_block_table.shape[1], pn, pi, po, ld_o, st)
+        rc = load().dsa_cache_evict(*cache, max_len_k, pm, ld, budget, int(sinks), int(recent), pt,
+                                    ld_t, new_block_table.shape[1], pn, pi, po, ld_o, st)
     _check(rc, "dsa_cache_evict")
 
 

@@ -15,7 +15,7 @@
 //   O^T [4 x 128 dims x 64 heads] += X[:, 0:512]^T P^T       16 MMAs, M128 N64 K16
 //
 // With the heads as rows the second product would be M = 64 too, at twice the
-// time (an M = 64 MMA costs about what an M = 128 one does).  The latents are read
+// time (an M = 64 MMA costs what an M = 128 one does).  The latents are read
 // from shared memory as they lie: rows of 64-column chunks are K-major for S^T
 // and, transposed, MN-major for O^T; P^T (a key's 64 heads in 128 bytes) is
 // written as an MN-major operand.
@@ -30,11 +30,16 @@
 // chunks in five parts with their own empty barriers).  P^T overwrites the RoPE
 // chunk of its tile, which the values do not need.  A part is reloaded as soon as
 // its product is done.  The two tiles are half a cycle apart: the softmax of one
-// and the reload of its latents run under the products of the other.  (One tile
-// of 128 keys, M = 128 for S^T, needs fewer MMA cycles (3300 against 3900 per 128
-// keys) but leaves the tensor cores idle through its softmax and reload: 5900
-// cycles per 128 keys.)  Two issuers, one for the S^T products and one for the
-// O^T products, so that neither waits behind the other.
+// and the reload of its latents run under the products of the other.  Two
+// issuers, one for the S^T products and one for the O^T products, so that neither
+// waits behind the other.
+//
+// What bounds it, on 64 sequences of 4K-128K: with up to 64 heads the cache's one
+// read (16 heads 790 us, 6.4 TB/s; 64 heads 893 us, 5.7 TB/s); with 128 the tensor
+// cores, whose products take 2600 cycles a tile as issued (S^T 1650, M = 64 at 46
+// cycles each; O^T 950): 1.52 ms, 800 TFLOP/s.  One tile of 128 keys at a time (M =
+// 128 for S^T) needs only 3300 tensor cycles per 128 keys, but idles through its
+// softmax and reload: 5900 cycles in all, 1.54 ms with 128 heads and 967 us with 64.
 //
 // The sequences' tiles stand in one line that is cut into equal pieces, one
 // per CTA (times the head groups, which read the same keys at the same time, so
@@ -404,7 +409,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           load();
           if (i > w.i0) {
             if (!mine || *version != seen_version) adopt();
-            over = weigh() > kMost;           // (a weight above it makes the sum so)
+            // (a weight above it makes the sum so; so does a NaN, which must not hide
+            // one from the vote)
+            over = !(weigh() <= kMost);
           }
         }
         // one vote for the group; it also takes its warps out together when a
@@ -575,11 +582,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Joins the parts of the sequences that were split: with the parts'
 // references m_i and M their maximum, out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
 // One CTA per (head, sequence), a thread four value dims of every kJoin-th part.
+// Every warp works out all the weights for itself (a lane has every 32nd part):
+// one round of loads, and no barrier before the parts' own loads.
 constexpr int kMaxParts = 160;
 template <int kJoin>
 __global__ void __launch_bounds__(128 * kJoin) combine_kernel(Params P) {
-  __shared__ float wt[kMaxParts];
-  __shared__ float tot[3];
   __shared__ float4 sums[kJoin > 1 ? kJoin - 1 : 1][128];
   const int h = blockIdx.x;
   const int b = blockIdx.y + gridDim.y * blockIdx.z;
@@ -591,66 +598,70 @@ __global__ void __launch_bounds__(128 * kJoin) combine_kernel(Params P) {
   const int r0 = t0 / per, r1 = (t0 + n - 1) / per;
   if (r0 == r1) return;
   const int parts = r1 - r0 + 1;
+  const int lane = threadIdx.x % 32, k = threadIdx.x / 128, d = threadIdx.x % 128;
   const int g = h / kHeads, hh = h % kHeads;
   auto slot = [&](int i) {
-    return (static_cast<int64_t>(r0 + i) * 2 + (i == 0 && t0 > r0 * per ? 1 : 0)) * P.groups + g;
+    return ((static_cast<int64_t>(r0 + i) * 2 + (i == 0 && t0 > r0 * per ? 1 : 0)) * P.groups + g) *
+               kHeads + hh;
   };
-  if (threadIdx.x < 32) {
-    float top = -INFINITY;
-#pragma unroll 1
-    for (int i = threadIdx.x; i < parts; i += 32) {
-      const float2 x = P.ml[slot(i) * kHeads + hh];
-      if (x.y != 0.f) top = fmaxf(top, x.x);          // a part without a weight has no reference
-    }
+  float2 x[kMaxParts / 32];
+  float top = -INFINITY;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    float l = 0.f;
-#pragma unroll 1
-    for (int i = threadIdx.x; i < parts; i += 32) {
-      const float2 x = P.ml[slot(i) * kHeads + hh];
-      const float f = x.y != 0.f ? exp2f(x.x - top) : 0.f;
-      wt[i] = f;
-      l += f * x.y;
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-    if (threadIdx.x == 0) {
-      tot[0] = l;
-      tot[1] = l == 0.f ? 0.f : 1.f / l;
-      tot[2] = top;
-    }
+  for (int u = 0; u < kMaxParts / 32; ++u) {
+    x[u] = make_float2(0.f, 0.f);
+    if (lane + 32 * u < parts) x[u] = P.ml[slot(lane + 32 * u)];
   }
-  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < kMaxParts / 32; ++u)
+    if (x[u].y != 0.f) top = fmaxf(top, x[u].x);      // a part without a weight has no reference
+#pragma unroll
+  for (int e = 16; e > 0; e >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, e));
+  float l = 0.f;
+#pragma unroll
+  for (int u = 0; u < kMaxParts / 32; ++u) {
+    const float f = x[u].y != 0.f ? exp2f(x[u].x - top) : 0.f;
+    l += f * x[u].y;
+    x[u].x = f;
+  }
+#pragma unroll
+  for (int e = 16; e > 0; e >>= 1) l += __shfl_xor_sync(0xffffffffu, l, e);
   // thread group k adds up every kJoin-th part; the groups' sums are then added
   // in their order
-  const int k = threadIdx.x / 128, d = threadIdx.x % 128;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](int i, float w) {
+    const float4 y = *reinterpret_cast<const float4*>(P.part + slot(i) * kDv + 4 * d);
+    const float f = __shfl_sync(0xffffffffu, w, i & 31);
+    o.x += f * y.x;
+    o.y += f * y.y;
+    o.z += f * y.z;
+    o.w += f * y.w;
+  };
 #pragma unroll 4
-  for (int i = k; i < parts; i += kJoin) {
-    const float4 x = *reinterpret_cast<const float4*>(P.part + (slot(i) * kHeads + hh) * kDv + 4 * d);
-    const float f = wt[i];
-    o.x += f * x.x;
-    o.y += f * x.y;
-    o.z += f * x.z;
-    o.w += f * x.w;
-  }
-  if (k > 0) sums[k - 1][d] = o;
-  __syncthreads();
-  if (k > 0) return;
+  for (int i = k; i < min(32, parts); i += kJoin) add(i, x[0].x);
+  if (parts > 32) {
 #pragma unroll
-  for (int j = 0; j < kJoin - 1; ++j) {
-    const float4 x = sums[j][d];
-    o.x += x.x;
-    o.y += x.y;
-    o.z += x.z;
-    o.w += x.w;
+    for (int u = 1; u < kMaxParts / 32; ++u)
+#pragma unroll kJoin > 1 ? 4 : 1
+      for (int i = 32 * u + k; i < min(32 * u + 32, parts); i += kJoin) add(i, x[u].x);
   }
-  const float inv = tot[1];
+  if (kJoin > 1) {
+    if (k > 0) sums[k - 1][d] = o;
+    __syncthreads();
+    if (k > 0) return;
+#pragma unroll
+    for (int j = 0; j < kJoin - 1; ++j) {
+      const float4 y = sums[j][d];
+      o.x += y.x;
+      o.y += y.y;
+      o.z += y.z;
+      o.w += y.w;
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   const int64_t row = static_cast<int64_t>(b) * P.H + h;
   *reinterpret_cast<uint2*>(P.out + row * kDv + 4 * d) =
       make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-  if (d == 0 && P.lse)
-    P.lse[row] = tot[0] == 0.f ? -INFINITY : (tot[2] + log2f(tot[0])) * kLn2;
+  if (d == 0 && P.lse) P.lse[row] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
 }
 
 constexpr int kMaxCtas = 148;

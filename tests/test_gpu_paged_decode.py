@@ -100,6 +100,22 @@ def test_nan_entry_stays_in_its_sequence():
     C.check_rows(lse[1], l, tol_l, "lse")
 
 
+def test_nan_head_stays_in_its_head():
+    """A head with a NaN query beside heads whose references have to move."""
+    c = C.Cache([700], page=16, H=16, seed=31)
+    ramp = torch.linspace(0, 60, 700)
+    x = (c.q[0, 3].float() / 24)[None, :] * ramp[:, None] + c.rows(0).float() * 0.2
+    for s in range(700):
+        c.pool[c.table[0, s // 16].long(), s % 16] = x[s].to(torch.bfloat16)
+    c.q[0, 2, 5] = float("nan")
+    out, lse = run(c)
+    assert torch.isnan(out[0, 2]).all() and torch.isnan(lse[0, 2])
+    o, l, tol, tol_l = C.attention64(c.q[0], c.rows(0), C.seen(700, 0, 0))
+    rest = [h for h in range(16) if h != 2]
+    C.check_rows(out[0, rest], o[rest], tol[rest], "out")
+    C.check_rows(lse[0, rest], l[rest], tol_l[rest], "lse")
+
+
 def test_strided_pages_shared_pages_and_table_slices():
     c = C.Cache([300, 290, 40], page=32, H=32, seed=27, layers=3, table_pad=5, spare=2)
     c.table[1, :9] = c.table[0, :9]             # a shared prefix of 288 entries
