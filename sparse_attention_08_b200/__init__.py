@@ -460,7 +460,7 @@ def dsa_masked_mha_fwd(q, k, v, idx, cu_seqlens_q, cu_seqlens_k, B, max_len_q, m
 
 
 class _On:
-    """The device and stream a call runs on: the given stream (a torch stream or
+    """The device (its number) and stream a call runs on: the given stream (a torch stream or
     a raw handle), or the device's current one.  Entered around the launch; on
     the current device and stream, the common case, that does nothing."""
 
@@ -469,10 +469,11 @@ class _On:
     def __init__(self, device, stream):
         import torch
         self._ctx = ()
-        if device.index != torch.cuda.current_device():
+        if device != torch.cuda.current_device():
             self._ctx = (torch.cuda.device(device),)
         if stream is None:
-            self.handle = torch.cuda.current_stream(device).cuda_stream
+            # (the handle alone: building a Stream object takes 2 us)
+            self.handle = torch._C._cuda_getCurrentRawStream(device)
         else:
             if not hasattr(stream, "cuda_stream"):
                 stream = torch.cuda.ExternalStream(int(stream), device=device)
@@ -490,60 +491,60 @@ class _On:
             c.__exit__(*exc)
 
 
-def _ten(t, dtype, shape, device, name):
-    """Checks a contiguous tensor (None passes) and returns its address.  shape:
-    the sizes, None where any will do."""
+def _ten(t, dtype, shape, dev, name):
+    """Checks a contiguous CUDA tensor of a shape on device number dev (None
+    passes) and returns its address."""
     if t is None:
         return None
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == dev and dev >= 0
+            and t.is_contiguous()):
+        return t.data_ptr()
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    have = t.shape
-    if len(have) != len(shape) or any(w is not None and h != w for h, w in zip(have, shape)):
-        want = tuple("any" if w is None else w for w in shape)
-        raise ValueError(f"{name} must have shape {want}, got {tuple(have)}")
-    return t.data_ptr()
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} must be on cuda:{max(dev, 0)}, got {t.device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _rows(t, dtype, B, least, device, name):
-    """Checks a matrix [B, >= least] whose rows are contiguous (None passes);
-    returns its address and row stride."""
+def _rows(t, dtype, B, least, dev, name):
+    """Checks a CUDA matrix [B, >= least] whose rows are contiguous (None
+    passes); returns its address and row stride."""
     if t is None:
         return None, 0
-    if t.dtype != dtype or t.device != device or t.dim() != 2 or t.shape[0] != B:
-        raise ValueError(f"{name} must be a {dtype} matrix of {B} rows on {device}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
+    if t.dtype != dtype or t.get_device() != dev or dev < 0 or t.dim() != 2 or t.shape[0] != B:
+        raise ValueError(f"{name} must be a {dtype} matrix of {B} rows on cuda:{max(dev, 0)}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
     n = t.shape[1]
     if n < least:
         raise ValueError(f"{name} must have at least {least} columns, got {n}")
-    if n > 1 and t.stride(1) != 1:
+    ld, step = t.stride()
+    if n > 1 and step != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return t.data_ptr(), (t.stride(0) if B > 1 else n)
+    return t.data_ptr(), (ld if B > 1 else n)
 
 
-def _cuda(t, name):
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
+def _dims(t, n, name):
+    if t.dim() != n:
+        raise ValueError(f"{name} must have {n} dims, got {t.dim()}")
+    return t.shape
 
 
 def _cache(kv_cache, block_table, seq_lens):
     """Checks the tensors of a paged cache; returns its arguments in the C ABI's
-    order, the number of sequences last, and the device."""
+    order, the number of sequences last, and the device's number."""
     import torch
-    dev = _cuda(kv_cache, "kv_cache")
-    if kv_cache.dtype != torch.bfloat16 or kv_cache.dim() != 3 or kv_cache.shape[2] != 576:
-        raise ValueError("kv_cache must be a torch.bfloat16 tensor [n_pages, page_size, 576]")
-    n_pages, page, _ = kv_cache.shape
+    n_pages, page, width = _dims(kv_cache, 3, "kv_cache")
+    if kv_cache.dtype != torch.bfloat16 or width != 576 or not kv_cache.is_cuda:
+        raise ValueError("kv_cache must be a CUDA torch.bfloat16 tensor [n_pages, page_size, 576]")
+    dev = kv_cache.get_device()
     stride, row, col = kv_cache.stride()
     if n_pages == 1:
         stride = page * 576
     if col != 1 or (page > 1 and row != 576):
         raise ValueError("kv_cache rows must lie one after the other within a page")
-    B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
+    (B,) = _dims(seq_lens, 1, "seq_lens")
     lens = _ten(seq_lens, torch.int32, (B,), dev, "seq_lens")
     table, ld = _rows(block_table, torch.int32, B, 1, dev, "block_table")
     return (kv_cache.data_ptr(), n_pages, page, stride, table, ld, block_table.shape[1], lens,
@@ -559,13 +560,12 @@ def dsa_window_mha_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, B, max_len_q, max_le
     import torch
     bf16, i32 = torch.bfloat16, torch.int32
     B = int(B)
-    dev = _cuda(q, "q")
-    pq = _ten(q, bf16, (None, None, None), dev, "q")
-    T_q, H, d_qk = q.shape
-    pk = _ten(k, bf16, (None, H, d_qk), dev, "k")
-    T_k = k.shape[0]
-    pv = _ten(v, bf16, (T_k, H, None), dev, "v")
-    d_v = v.shape[2]
+    T_q, H, d_qk = _dims(q, 3, "q")
+    T_k, d_v = _dims(k, 3, "k")[0], _dims(v, 3, "v")[2]
+    dev = q.get_device()
+    pq = _ten(q, bf16, (T_q, H, d_qk), dev, "q")
+    pk = _ten(k, bf16, (T_k, H, d_qk), dev, "k")
+    pv = _ten(v, bf16, (T_k, H, d_v), dev, "v")
     po = _ten(out, bf16, (T_q, H, d_v), dev, "out")
     pl = _ten(lse, torch.float32, (T_q, H), dev, "lse")
     cq = _ten(cu_seqlens_q, i32, (B + 1,), dev, "cu_seqlens_q")
@@ -594,18 +594,20 @@ def dsa_paged_mla_decode(q, kv_cache, block_table, seq_lens, max_len_k, sm_scale
     max_len_k = int(max_len_k)
     cache, dev = _cache(kv_cache, block_table, seq_lens)
     B = cache[-1]
-    pq = _ten(q, torch.bfloat16, (B, None, None), dev, "q")
-    _, H, d_qk = q.shape
-    po = _ten(out, torch.bfloat16, (B, H, None), dev, "out")
+    _, H, d_qk = _dims(q, 3, "q")
+    d_v = _dims(out, 3, "out")[2]
+    pq = _ten(q, torch.bfloat16, (B, H, d_qk), dev, "q")
+    po = _ten(out, torch.bfloat16, (B, H, d_v), dev, "out")
     pl = _ten(lse, torch.float32, (B, H), dev, "lse")
-    pw = _ten(workspace, torch.uint8, (None,), dev, "workspace")
+    pw = None if workspace is None else _ten(workspace, torch.uint8, (workspace.numel(),), dev,
+                                             "workspace")
     lib = load()
     with _On(dev, stream) as st:
         if pw is None:
             nbytes = lib.dsa_paged_mla_decode_workspace_size(B, H, max_len_k)
-            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
             pw = workspace.data_ptr()
-        rc = lib.dsa_paged_mla_decode(pq, *cache, max_len_k, H, d_qk, out.shape[2], int(window),
+        rc = lib.dsa_paged_mla_decode(pq, *cache, max_len_k, H, d_qk, d_v, int(window),
                                       int(sinks), float(sm_scale), po, pl, pw, workspace.numel(),
                                       st)
     _check(rc, "dsa_paged_mla_decode")
@@ -622,8 +624,8 @@ def dsa_paged_attn_mass(q, kv_cache, block_table, seq_lens, lse, max_len_k, sm_s
     max_len_k = int(max_len_k)
     cache, dev = _cache(kv_cache, block_table, seq_lens)
     B = cache[-1]
-    pq = _ten(q, torch.bfloat16, (B, None, None), dev, "q")
-    _, H, d_qk = q.shape
+    _, H, d_qk = _dims(q, 3, "q")
+    pq = _ten(q, torch.bfloat16, (B, H, d_qk), dev, "q")
     pl = _ten(lse, f32, (B, H), dev, "lse")
     po, ld = _rows(mass_out, f32, B, max_len_k, dev, "mass_out")
     pi, ld_in = _rows(mass_in, f32, B, max_len_k, dev, "mass_in")

@@ -321,8 +321,10 @@ __global__ void __launch_bounds__(256, 4) move_kernel(Params P, uint8_t* pool, i
 
 template <int C>
 cudaError_t launch_select(const Params& P, size_t smem, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(select_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  // (the most that rows of up to 262144 entries take)
+  constexpr int kMostSmem = kWarps * (262144 / (kClusterC * kWarps) / 32 * 33) * 4;
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(select_kernel<C>, kMostSmem, allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(P.c.B) * C);

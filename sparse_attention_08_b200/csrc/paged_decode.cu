@@ -703,9 +703,8 @@ cudaError_t launch_paged_decode(const CUtensorMap& tq, const CUtensorMap& tx,
   ws += static_cast<size_t>(2) * P.pieces * P.groups * kHeads * 8;
   P.part = reinterpret_cast<float*>(ws);
   P.err = err;
-  cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(kSmem));
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(paged_decode_kernel, static_cast<int>(kSmem), allowed);
   if (e != cudaSuccess) return e;
   paged_decode_kernel<<<static_cast<unsigned>(P.pieces * P.groups), kThreads, kSmem, s>>>(tq, tx, P);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

@@ -284,8 +284,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 cudaError_t launch_paged_mass(const CUtensorMap* tq, int launches, const CUtensorMap& tx,
                               const PagedMassArgs& a, const DevErr* err, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(paged_mass_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(paged_mass_kernel, 232448, allowed);
   if (e != cudaSuccess) return e;
   for (int i = 0; i < launches; ++i) {
     Params P;

@@ -597,9 +597,8 @@ cudaError_t launch_window_mha(const CUtensorMap& tq, const CUtensorMap& tk, cons
   P.out = reinterpret_cast<__nv_bfloat16*>(a.out);
   P.lse = a.lse;
   P.err = err;
-  cudaError_t e = cudaFuncSetAttribute(window_mha_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(kSmem));
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(window_mha_kernel, static_cast<int>(kSmem), allowed);
   if (e != cudaSuccess) return e;
   const unsigned grid = static_cast<unsigned>(P.items < a.num_sms ? P.items : a.num_sms);
   window_mha_kernel<<<grid, kThreads, kSmem, s>>>(tq, tk, tv, P);
