@@ -82,8 +82,8 @@ constexpr int kWarps = kLoaders + 2 + kSoft;
 constexpr int kThreads = 32 * kWarps;
 constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;         // TMEM slot, plan scratch
 constexpr uint32_t kOffRef = (kOffMisc + 16 + (kWarps + 4) * 4 + 127) / 128 * 128;   // -m[64], alpha[64]
-constexpr uint32_t kOffRed = kOffRef + 2 * kHeads * 4;        // [8][64]
-constexpr uint32_t kSmem = kOffRed + 8 * kHeads * 4 + 1024;
+constexpr uint32_t kOffRed = kOffRef + 2 * kHeads * 4;        // [2][8][64]
+constexpr uint32_t kSmem = kOffRed + 16 * kHeads * 4 + 1024;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0;                         // + 64 * (dims / 128)
 constexpr uint32_t kColS = 256;                       // lanes 0-15 of each 32 for slot 0, 16-31 for slot 1
@@ -102,7 +102,7 @@ struct Params {
   __nv_bfloat16* out;   // [B, H, 512]
   float* lse;           // [B, H], nullable
   int32_t* plan;        // workspace: [B] first tile of each sequence, [B] tiles per piece
-  float2* ml;           // workspace: [2 * pieces * groups][64] reference, sum
+  float4* ml;           // workspace: [2 * pieces * groups][64] reference, sums
   float* part;          // workspace: [2 * pieces * groups][64][512] unnormalised O
   DevErr err;
 };
@@ -353,11 +353,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
 #pragma unroll 1
     for (int seg = 0; w.next(seg == 0); ++seg) {
-      float2 l[4], rr[4];         // sums of the weights, and the references they are over
+      // Sums of the weights, and of the weights as rounded to bf16 for the product
+      // (O^T is divided by the latter, so that its weights add up to one exactly),
+      // and the references they are over.
+      float2 l[4], lr[4], rr[4];
       uint32_t seen_version = 0;
       bool mine = false;          // a tile of this segment was this group's
 #pragma unroll
-      for (int e = 0; e < 4; ++e) l[e] = rr[e] = make_float2(0.f, 0.f);
+      for (int e = 0; e < 4; ++e) l[e] = lr[e] = rr[e] = make_float2(0.f, 0.f);
 #pragma unroll 1
       for (int i = w.i0; i < w.i1; ++i, ++n) {
         if (static_cast<int>(n & 1) != grp || !ok) continue;
@@ -384,8 +387,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float2 m = *reinterpret_cast<const float2*>(ref + hq + 8 * e);
-            if (mine)
-              l[e] = __fmul2_rn(l[e], make_float2(fast_exp2(m.x - rr[e].x), fast_exp2(m.y - rr[e].y)));
+            if (mine) {
+              const float2 f = make_float2(fast_exp2(m.x - rr[e].x), fast_exp2(m.y - rr[e].y));
+              l[e] = __fmul2_rn(l[e], f);
+              lr[e] = __fmul2_rn(lr[e], f);
+            }
             rr[e] = m;
           }
           seen_version = *version;
@@ -475,8 +481,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 4; ++e) {
           l[e] = __fadd2_rn(l[e], __fadd2_rn(ya[e], yb[e]));
           const uint32_t at = ((4 * half + e) ^ (lane / 4)) * 16 + 4 * (lane & 3);
-          *reinterpret_cast<uint32_t*>(tile + kOffP + ra * 128 + at) = pack_bf16x2(ya[e].x, ya[e].y);
-          *reinterpret_cast<uint32_t*>(tile + kOffP + rb * 128 + at) = pack_bf16x2(yb[e].x, yb[e].y);
+          const uint32_t pa = pack_bf16x2(ya[e].x, ya[e].y), pb = pack_bf16x2(yb[e].x, yb[e].y);
+          *reinterpret_cast<uint32_t*>(tile + kOffP + ra * 128 + at) = pa;
+          *reinterpret_cast<uint32_t*>(tile + kOffP + rb * 128 + at) = pb;
+          lr[e] = __fadd2_rn(lr[e], __fadd2_rn(make_float2(__uint_as_float(pa << 16), __uint_as_float(pa & 0xFFFF0000u)),
+                                               make_float2(__uint_as_float(pb << 16), __uint_as_float(pb & 0xFFFF0000u))));
         }
         // an unseen row of the tile holds whatever its memory held: its
         // weight is 0, and so must its value be (0 * NaN is not)
@@ -504,33 +513,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float2 t = l[e];
+        float4 t = make_float4(l[e].x, l[e].y, lr[e].x, lr[e].y);
         if (mine) {
           const float2 m = *reinterpret_cast<const float2*>(ref + hq + 8 * e);
-          t = __fmul2_rn(t, make_float2(fast_exp2(m.x - rr[e].x), fast_exp2(m.y - rr[e].y)));
+          const float2 f = make_float2(fast_exp2(m.x - rr[e].x), fast_exp2(m.y - rr[e].y));
+          t = make_float4(t.x * f.x, t.y * f.y, t.z * f.x, t.w * f.y);
         }
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) {
           t.x += __shfl_xor_sync(0xffffffffu, t.x, d);
           t.y += __shfl_xor_sync(0xffffffffu, t.y, d);
+          t.z += __shfl_xor_sync(0xffffffffu, t.z, d);
+          t.w += __shfl_xor_sync(0xffffffffu, t.w, d);
         }
-        if (lane < 4) *reinterpret_cast<float2*>(red + (4 * grp + sp) * kHeads + hq + 8 * e) = t;
+        if (lane < 4) {
+          float* to = red + (4 * grp + sp) * kHeads + hq + 8 * e;
+          *reinterpret_cast<float2*>(to) = make_float2(t.x, t.y);
+          *reinterpret_cast<float2*>(to + 8 * kHeads) = make_float2(t.z, t.w);
+        }
       }
       named_bar_sync(3, kSoftThreads);
       const int tiles = max(w.k.n, 1);
       const bool whole = w.i0 == 0 && w.i1 == tiles;
       const int64_t slot = (static_cast<int64_t>(piece) * 2 + (seg == 0 ? 0 : 1)) * P.groups + g;
       if (tid < heads) {
-        float sum = 0.f;
+        float sum = 0.f, sumr = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum += red[e * kHeads + tid];
+        for (int e = 0; e < 8; ++e) {
+          sum += red[e * kHeads + tid];
+          sumr += red[(8 + e) * kHeads + tid];
+        }
         const int64_t at = static_cast<int64_t>(w.b) * P.H + g * kHeads + tid;
         if (whole) {
           if (P.lse) P.lse[at] = sum == 0.f ? -INFINITY : (log2f(sum) - ref[tid]) * kLn2;
         } else {
-          P.ml[slot * kHeads + tid] = make_float2(-ref[tid], sum);
+          P.ml[slot * kHeads + tid] = make_float4(-ref[tid], sum, sumr, 0.f);
         }
-        alpha[tid] = sum == 0.f ? 0.f : 1.f / sum;
+        alpha[tid] = sumr == 0.f ? 0.f : 1.f / sumr;
       }
       if (w.i0 == 0 && g == 0 && tid == 0)
         P.plan[w.b] = piece * start.per + start.per - w.left - (w.i1 - w.i0);
@@ -604,11 +623,11 @@ __global__ void __launch_bounds__(128 * kJoin) combine_kernel(Params P) {
     return ((static_cast<int64_t>(r0 + i) * 2 + (i == 0 && t0 > r0 * per ? 1 : 0)) * P.groups + g) *
                kHeads + hh;
   };
-  float2 x[kMaxParts / 32];
+  float4 x[kMaxParts / 32];
   float top = -INFINITY;
 #pragma unroll
   for (int u = 0; u < kMaxParts / 32; ++u) {
-    x[u] = make_float2(0.f, 0.f);
+    x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (lane + 32 * u < parts) x[u] = P.ml[slot(lane + 32 * u)];
   }
 #pragma unroll
@@ -616,15 +635,19 @@ __global__ void __launch_bounds__(128 * kJoin) combine_kernel(Params P) {
     if (x[u].y != 0.f) top = fmaxf(top, x[u].x);      // a part without a weight has no reference
 #pragma unroll
   for (int e = 16; e > 0; e >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, e));
-  float l = 0.f;
+  float l = 0.f, lr = 0.f;
 #pragma unroll
   for (int u = 0; u < kMaxParts / 32; ++u) {
     const float f = x[u].y != 0.f ? exp2f(x[u].x - top) : 0.f;
     l += f * x[u].y;
+    lr += f * x[u].z;
     x[u].x = f;
   }
 #pragma unroll
-  for (int e = 16; e > 0; e >>= 1) l += __shfl_xor_sync(0xffffffffu, l, e);
+  for (int e = 16; e > 0; e >>= 1) {
+    l += __shfl_xor_sync(0xffffffffu, l, e);
+    lr += __shfl_xor_sync(0xffffffffu, lr, e);
+  }
   // thread group k adds up every kJoin-th part; the groups' sums are then added
   // in their order
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -657,7 +680,7 @@ __global__ void __launch_bounds__(128 * kJoin) combine_kernel(Params P) {
       o.w += y.w;
     }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float inv = lr == 0.f ? 0.f : 1.f / lr;
   const int64_t row = static_cast<int64_t>(b) * P.H + h;
   *reinterpret_cast<uint2*>(P.out + row * kDv + 4 * d) =
       make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
@@ -683,7 +706,7 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 size_t paged_decode_workspace_bytes(int B, int H, int max_len_k) {
   const size_t slots = static_cast<size_t>(2) * pieces_of(B, H, max_len_k) * groups_of(H);
-  return up256((static_cast<size_t>(B) + 1) * 4) + slots * kHeads * (8 + kDv * 4);
+  return up256((static_cast<size_t>(B) + 1) * 4) + slots * kHeads * (16 + kDv * 4);
 }
 
 cudaError_t launch_paged_decode(const CUtensorMap& tq, const CUtensorMap& tx,
@@ -699,8 +722,8 @@ cudaError_t launch_paged_decode(const CUtensorMap& tq, const CUtensorMap& tx,
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   P.plan = reinterpret_cast<int32_t*>(ws);
   ws += up256((static_cast<size_t>(a.cache.B) + 1) * 4);
-  P.ml = reinterpret_cast<float2*>(ws);
-  ws += static_cast<size_t>(2) * P.pieces * P.groups * kHeads * 8;
+  P.ml = reinterpret_cast<float4*>(ws);
+  ws += static_cast<size_t>(2) * P.pieces * P.groups * kHeads * 16;
   P.part = reinterpret_cast<float*>(ws);
   P.err = err;
   static std::atomic<uint64_t> allowed{0};

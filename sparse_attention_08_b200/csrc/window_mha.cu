@@ -407,7 +407,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int p = x.off + i;
       const int first = P.window > 0 ? max(0, p - P.window + 1) : 0;
       float m = 0.f;              // the row's reference
-      float2 l = make_float2(0.f, 0.f);
+      // sums of the weights, and of the weights as rounded to bf16 for the product:
+      // O is divided by the latter, so that its weights add up to one exactly (a
+      // row that sees one key, or all but one from afar, gets that key's value)
+      float2 l = make_float2(0.f, 0.f), lr = l;
 #pragma unroll 1
       for (int k = 0; k < x.n; ++k) {
         const int j = x.key_tile(k);
@@ -426,12 +429,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         uint32_t pk[64];
-        float2 sum;
+        float2 sum, sumr;
         // the weights over the reference m: 32 columns at a time, the next ones
         // arriving under this one's arithmetic
         auto weigh = [&]() {
           const float2 s2 = make_float2(P.scale_log2, P.scale_log2), n2 = make_float2(-m, -m);
-          sum = make_float2(0.f, 0.f);
+          sum = sumr = make_float2(0.f, 0.f);
           auto part = [&](int c, uint32_t (&v)[32]) {
             if (!whole) {
 #pragma unroll
@@ -444,7 +447,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                           s2, n2);
               const float2 w = make_float2(fast_exp2(y.x), fast_exp2(y.y));
               sum = __fadd2_rn(sum, w);
-              pk[16 * c + e] = pack_bf16x2(w.x, w.y);
+              const uint32_t b = pack_bf16x2(w.x, w.y);
+              sumr = __fadd2_rn(sumr, make_float2(__uint_as_float(b << 16), __uint_as_float(b & 0xFFFF0000u)));
+              pk[16 * c + e] = b;
             }
           };
           uint32_t va[32], vb[32];
@@ -485,6 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             al = fresh ? 0.f : fast_exp2(m - mx);
             m = mx;
             l = __fmul2_rn(l, make_float2(al, al));
+            lr = __fmul2_rn(lr, make_float2(al, al));
           }
           // O is complete up to the tile before: its product was issued before
           // these scores'
@@ -502,6 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           weigh();
         }
         l = __fadd2_rn(l, sum);
+        lr = __fadd2_rn(lr, sumr);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t w[32];
@@ -522,8 +529,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       ++no;
       tc_fence_after();
-      const float total = l.x + l.y;
-      const float inv = total == 0.f ? 0.f : 1.f / total;
+      const float total = l.x + l.y, rounded = lr.x + lr.y;
+      const float inv = rounded == 0.f ? 0.f : 1.f / rounded;
       // Eight lanes trade their rows' 16-byte pieces, so that a store covers whole
       // lines (a row's neighbour lies H * 256 bytes away: with a lane per row every
       // store touched 32 lines, 4500 cycles for the tile).

@@ -90,6 +90,14 @@ def test_very_negative_scores():
     check(c, *run(c))
 
 
+def test_a_single_entry_gives_its_value():
+    """Weights that add up to one exactly: a token that sees one entry gets its value's bits."""
+    c = C.Cache([1, 77, 300], page=16, H=16, seed=32)
+    out, _ = run(c, window=1)
+    for b, n in enumerate(c.lens_list):
+        assert torch.equal(out[b].cpu(), c.rows(b)[n - 1, :512].expand(16, -1))
+
+
 def test_nan_entry_stays_in_its_sequence():
     c = C.Cache([200, 200], page=16, H=16, seed=26)
     c.pool[c.table[0, 3].long(), 2] = float("nan")

@@ -2,8 +2,8 @@
 
 Tolerances: those of tests/paged_cases.py with 192 dims in a score: a score is off
 by at most d = 192 * 2^-23 * scale * sum |q||k| (and 2^-21 of its size), a weight
-by exp(2 d) and its rounding to bf16 (2^-8; the normalising sum is of the
-unrounded weights), the output by its own rounding (2^-8)."""
+by exp(2 d) and its rounding to bf16 (2^-8, and 2^-8 again in the normalising sum,
+which is of the rounded weights), the output by its own rounding (2^-8)."""
 import numpy as np
 import pytest
 import torch
@@ -109,6 +109,14 @@ def test_scores_far_from_zero(shift):
         out, lse = call(q, k, v, cu_q, cu_k, lens_q, [400], window, sinks)
         assert_no_device_error()
         check(q, k, v, cu_q, cu_k, out, lse, window, sinks)
+
+
+def test_a_single_key_gives_its_value():
+    """Weights that add up to one exactly: a row that sees one key gets its value's bits."""
+    q, k, v, cu_q, cu_k, lens_q = make([300], None, 3, seed=88, q_mul=3.0)
+    out, _ = call(q, k, v, cu_q, cu_k, lens_q, [300], 1, 0)
+    assert_no_device_error()
+    assert torch.equal(out.cpu(), v)
 
 
 def test_another_sequences_nan_stays_there():
