@@ -29,8 +29,19 @@
 //              first and O rescaled.
 // TMEM: S (and P) at columns 0 and 128, O at 256 and 384.
 //
-// Bound by the tensor cores: 20 MMAs of 64 cycles per tile pair of 128 x 128,
-// of which the softmax's exponentials (128 x 128 at 16 a cycle) take four fifths.
+// Two bounds lie close together: a step's 40 MMAs take 2560 cycles, its exponentials
+// (2 x 128 x 128 at 16 a cycle) 2050.  What a step takes is the turn's way around:
+// twice (P V 550, keys' wait 165, S 940, hand-over 380), 4030 cycles, under which a
+// softmax of 1850 is hidden.  Measured at L = 4096, 128 heads: causal 622 us
+// (1.10 PFLOP/s, the tensor cores' share 0.65), window 1024 with four first tokens
+// 364 us (0.83), where an item's ends cost about 2 steps (the read-out, and
+// keys that come late since the ring holds 1.6 key tiles).
+//
+// Tried: the first 96 keys' weights handed over by themselves (2 % slower: its vote,
+// store and barrier cost more than the 380 cycles of products it hides), the turn
+// given back before the last S MMAs (5-10 % slower), the first tokens' tile cut to
+// the MMAs it needs (even), a part of the exponentials on the FMA pipe as a polynomial
+// (1545 -> 1445 cycles for one softmax alone, 2500 -> 2400-2700 for two at once).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -85,7 +96,7 @@ struct Params {
   int B, H;
   int pairs;                // query-tile pairs per sequence slot
   int window, sinks;        // window 0: no limit
-  int items;
+  int items, rounds;        // rounds: items per CTA
   float scale_log2;
   __nv_bfloat16* out;
   float* lse;
@@ -96,33 +107,14 @@ struct Params {
 struct Item {
   int b, h, q0, rows, tiles;   // tiles: query tiles, 1 or 2 (0: nothing here)
   int cq, ck, len_k, off;      // query i of the sequence sits at position off + i
-  int a, w0, n;                // key tiles: the first a, then from w0 on; n in all
-  __device__ __forceinline__ int key_tile(int i) const { return i < a ? i : w0 + (i - a); }
+  int a, w0;                   // key tiles: the first a, then from w0 on
+  int n;                       // steps; one key tile each, but for
+  int pair;                    // 1: the last step, with query tile 0 on tile w0 - 1, 1 on the next
+  __device__ __forceinline__ int key_tile(int i, int t) const {
+    return pair != 0 && i == n - 1 && t == 0 ? w0 - 1 : i < a ? i : w0 + (i - a);
+  }
+  __device__ __forceinline__ bool split(int i) const { return pair != 0 && i == n - 1; }
 };
-
-__device__ __forceinline__ Item item_of(const Params& P, uint32_t i) {
-  Item x;
-  if (i >= static_cast<uint32_t>(P.items)) i = 0;    // (looked up ahead, past the last: not used)
-  // the query tiles of a head are neighbours: they share its keys in L2; the
-  // last ones, which may have the most keys, go first
-  const uint32_t bh = i / static_cast<uint32_t>(P.pairs);
-  x.b = static_cast<int>(bh / static_cast<uint32_t>(P.H));
-  x.h = static_cast<int>(bh) - x.b * P.H;
-  x.q0 = (P.pairs - 1 - static_cast<int>(i - bh * P.pairs)) * (2 * kBM);
-  x.cq = __ldg(P.cu_q + x.b);
-  x.ck = __ldg(P.cu_k + x.b);
-  const int len_q = __ldg(P.cu_q + x.b + 1) - x.cq;
-  x.len_k = __ldg(P.cu_k + x.b + 1) - x.ck;
-  x.off = x.len_k - len_q;
-  x.rows = min(2 * kBM, len_q - x.q0);
-  x.tiles = x.rows <= 0 || x.off < 0 ? 0 : (x.rows > kBM ? 2 : 1);
-  const int p0 = x.off + x.q0, p1 = p0 + x.rows - 1;
-  const int lo = P.window > 0 ? max(0, p0 - P.window + 1) : 0;
-  x.a = (min(P.sinks, lo) + kBN - 1) / kBN;
-  x.w0 = max(lo / kBN, x.a);
-  x.n = x.a + p1 / kBN + 1 - x.w0;
-  return x;
-}
 
 // What query tile t (rows of one accumulator) sees of key tile j.
 struct Rows {
@@ -140,6 +132,46 @@ struct Rows {
            (P.window == 0 || j * kBN > p1 - P.window || j * kBN + kBN <= P.sinks);
   }
 };
+
+// A CTA's n-th item.  Every other round of the grid goes backwards: the items' work
+// repeats with the heads, and in one direction a CTA would keep meeting the long ones
+// (causal, L = 4096, 128 heads: the busiest CTA has 1.23 times the mean, this way 1.07).
+__device__ __forceinline__ Item item_of(const Params& P, int n) {
+  Item x;
+  const uint32_t c = (n & 1) != 0 ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+  uint32_t i = static_cast<uint32_t>(n) * gridDim.x + c;
+  const bool none = i >= static_cast<uint32_t>(P.items);   // (the last round's rest, or past it)
+  if (none) i = 0;
+  // the query tiles of a head are neighbours: they share its keys in L2; the
+  // last ones, which may have the most keys, go first
+  const uint32_t bh = i / static_cast<uint32_t>(P.pairs);
+  x.b = static_cast<int>(bh / static_cast<uint32_t>(P.H));
+  x.h = static_cast<int>(bh) - x.b * P.H;
+  x.q0 = (P.pairs - 1 - static_cast<int>(i - bh * P.pairs)) * (2 * kBM);
+  x.cq = __ldg(P.cu_q + x.b);
+  x.ck = __ldg(P.cu_k + x.b);
+  const int len_q = __ldg(P.cu_q + x.b + 1) - x.cq;
+  x.len_k = __ldg(P.cu_k + x.b + 1) - x.ck;
+  x.off = x.len_k - len_q;
+  x.rows = min(2 * kBM, len_q - x.q0);
+  if (none) x.rows = 0;
+  x.tiles = x.rows <= 0 || x.off < 0 ? 0 : (x.rows > kBM ? 2 : 1);
+  const int p0 = x.off + x.q0, p1 = p0 + x.rows - 1;
+  const int lo = P.window > 0 ? max(0, p0 - P.window + 1) : 0;
+  x.a = (min(P.sinks, lo) + kBN - 1) / kBN;
+  x.w0 = max(lo / kBN, x.a);
+  x.n = x.a + p1 / kBN + 1 - x.w0;
+  // A window's first key tile is query tile 0's alone, its last one query tile 1's:
+  // they make one step, the last.  (One after the other they left a query tile idle at
+  // each end, and the next item's keys came late: the ring held the other's last
+  // tiles.  L = 4096, 128 heads: window 128 176 -> 163 us, 1024 368 -> 364.)
+  x.pair = x.tiles == 2 && !Rows(P, x, 1).any(P, x.w0) && !Rows(P, x, 0).any(P, p1 / kBN) ? 1 : 0;
+  if (x.pair != 0) {
+    ++x.w0;
+    --x.n;
+  }
+  return x;
+}
 
 // Bits [lo, hi) of a 32-bit word.
 __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
@@ -202,23 +234,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ TMA
     uint32_t box = 0, unit = 0, nq0 = 0, nq1 = 0;
     bool ok = true;
-    // one unit (a key or a value tile): its boxes, announced on its barrier
-    auto load = [&](const CUtensorMap* m, int boxes, int h, int row) {
+    // one unit (a step's key or value tile, or two of them): its boxes, announced on its barrier
+    auto load = [&](const CUtensorMap* m, int each, int h, int row, int second) {
+      const int boxes = second < 0 ? each : 2 * each;
 #pragma unroll 1
       for (int c = 0; ok && c < boxes; ++c, ++box) {
         ok = all_wait(empty(box), ((box / kRing) & 1) ^ 1, P.err);
         if (!ok) break;
         if (lane == 0) {
           if (c == 0) mbar_arrive_expect_tx(full(unit), static_cast<uint32_t>(boxes) * kBox);
-          tma_load_3d(sbase + kOffRing + (box & (kRing - 1)) * kBox, m, 64 * c, h, row, full(unit));
+          tma_load_3d(sbase + kOffRing + (box & (kRing - 1)) * kBox, m,
+                      64 * (c < each ? c : c - each), h, c < each ? row : second, full(unit));
         }
         __syncwarp();
       }
       if (ok) ++unit;
     };
 #pragma unroll 1
-    for (int i = blockIdx.x; ok && i < P.items; i += gridDim.x) {
-      const Item x = item_of(P, i);
+    for (int it = 0; ok && it < P.rounds; ++it) {
+      const Item x = item_of(P, it);
       // (more queries than keys: there is no such sequence)
       if (x.off < 0 && x.rows > 0 && lane == 0) raise_error(P.err, kErrBounds);
       if (x.tiles == 0) continue;
@@ -238,11 +272,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       queries(0);
 #pragma unroll 1
       for (int j = 0; ok && j < x.n; ++j) {
-        const int row = x.ck + x.key_tile(j) * kBN;
-        load(&tk, 3, x.h, row);
+        const int row = x.ck + x.key_tile(j, 0) * kBN;
+        const int second = x.split(j) ? x.ck + x.key_tile(j, 1) * kBN : -1;
+        load(&tk, 3, x.h, row, second);
         // (query tile 1 is done with the item before later than tile 0)
         if (j == 0 && x.tiles > 1) queries(1);
-        load(&tv, 2, x.h, row);
+        load(&tv, 2, x.h, row, second);
       }
     }
     // after a failure, let the copies in flight land before the memory goes
@@ -271,18 +306,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     // The next item is looked up while this one's first softmax runs: at an item's
     // end the lookup (loads, divisions, code not in the cache) cost 3000 cycles.
-    Item nx = item_of(P, blockIdx.x);
+    Item nx = item_of(P, 0);
 #pragma unroll 1
-    for (int it = blockIdx.x; ok && it < P.items;) {
+    for (int it = 0; ok && it < P.rounds;) {
       const Item x = nx;
-      it += gridDim.x;
+      ++it;
       if (x.tiles == 0) {
         nx = item_of(P, it);
         continue;
       }
       const Rows mine(P, x, t), other(P, x, t ^ 1);
       auto needs = [&](int u, int i) -> bool {
-        return u < x.tiles && (u == t ? mine : other).any(P, x.key_tile(i));
+        return u < x.tiles && (u == t ? mine : other).any(P, x.key_tile(i, u));
       };
       int last = x.n - 1;         // the tile's last key tile
       while (t < x.tiles && last > 0 && !needs(t, last)) --last;
@@ -297,14 +332,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool pv = i >= 0 && needs(t, i), sn = i + 1 < x.n && needs(t, i + 1);
         // (a step in which the other query tile has no weights to wait for is no turn)
         const bool both = pv && needs(t ^ 1, i);
-        const uint32_t vb = uniform(box), kb = uniform(box + (i >= 0 ? 2 : 0));
+        // the step's value boxes, the next one's key boxes; in a split step the query
+        // tile's own ones, and after them or before them the other's
+        const uint32_t vs = i >= 0 && x.split(i) ? 2 : 0, ks = x.split(i + 1) ? 3 : 0;
+        const uint32_t v0 = box, k0 = box + (i >= 0 ? 2 + vs : 0);
+        const uint32_t vb = uniform(v0 + vs * t), kb = uniform(k0 + ks * t);
+        // Values and the turn first: the weights then meet an issuer with no other wait
+        // left (each one costs it 200 cycles, there or not).  The next keys after the
+        // product: they come half a step later, when the other query tile has let go of
+        // the boxes (waited for first: causal 654 against 622 us).
         if (i >= 0) {
           ok = all_wait(full(unit), (unit / 4) & 1, P.err);
           if (!ok) break;
           ++unit;
           // value rows past the sequence are another's (or unwritten memory):
           // their weights are 0, and so must they be (0 * NaN is not)
-          const int rem = x.len_k - x.key_tile(i) * kBN;
+          const int rem = x.len_k - x.key_tile(i, t) * kBN;
           if (pv && rem < kBN && x.ck + x.len_k < P.total_k) {
 #pragma unroll 1
             for (int e = rem * 8 + lane; e < kBN * 8; e += 32) {
@@ -315,17 +358,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_smem();
             __syncwarp();
           }
-          if (pv) {
-            ok = all_wait(p_full(t), ns & 1, P.err);
-            ++ns;
-          }
-          if (ok && both) {
-            ok = all_wait(turn(t), (turns & 1) ^ (t == 0 ? 1u : 0u), P.err);
-            ++turns;
-          }
+        }
+        if (both) {
+          ok = all_wait(turn(t), (turns & 1) ^ (t == 0 ? 1u : 0u), P.err);
           if (!ok) break;
-          tc_fence_after();
-          if (pv && elect_one()) {
+          ++turns;
+        }
+        if (pv) {
+          ok = all_wait(p_full(t), ns & 1, P.err);
+          if (!ok) break;
+          ++ns;
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          if (pv) {
             const uint64_t b0 = dV + (((vb & (kRing - 1)) * kBox) >> 4);
             if ((vb & (kRing - 1)) != kRing - 1) {
 #pragma unroll
@@ -344,17 +390,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_commit(empty(vb));
             mma_commit(empty(vb + 1));
           }
-          __syncwarp();
-          if (pv) more = 1;
-          // boxes that this query tile has no use for
-          if (!pv && lane < 2) mbar_arrive(empty(vb + lane));
         }
+        __syncwarp();
         if (i + 1 < x.n) {
           ok = all_wait(full(unit), (unit / 4) & 1, P.err);
           if (!ok) break;
           ++unit;
-          tc_fence_after();
-          if (sn && elect_one()) {
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          if (sn) {
 #pragma unroll
             for (int c = 0; c < 3; ++c) {
               const uint64_t b = dR + ((((kb + c) & (kRing - 1)) * kBox) >> 4);
@@ -369,11 +414,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_commit(empty(kb + 1));
             mma_commit(empty(kb + 2));
           }
-          __syncwarp();
-          if (!sn && lane < 3) mbar_arrive(empty(kb + lane));
         }
+        __syncwarp();
+        if (pv) more = 1;
+        // boxes that this query tile has no use for
+        if (i >= 0 && !pv && lane < 2) mbar_arrive(empty(vb + lane));
+        if (i + 1 < x.n && !sn && lane < 3) mbar_arrive(empty(kb + lane));
+        if (lane < vs) mbar_arrive(empty(v0 + vs * (1 - t) + lane));
+        if (lane < ks) mbar_arrive(empty(k0 + ks * (1 - t) + lane));
         if (both && lane == 0) mbar_arrive(turn(t ^ 1));
-        box = kb + (i + 1 < x.n ? 3 : 0);
+        box = k0 + (i + 1 < x.n ? 3 + ks : 0);
         if (i < 0) nx = item_of(P, it);
       }
     }
@@ -392,11 +442,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t oc = tmem + lane_base + kColO + 128u * t;
     uint32_t ns = 0, no = 0;
     bool ok = true;
-    Item nx = item_of(P, blockIdx.x);
+    Item nx = item_of(P, 0);
 #pragma unroll 1
-    for (int it = blockIdx.x; ok && it < P.items;) {
+    for (int it = 0; ok && it < P.rounds;) {
       const Item x = nx;
-      it += gridDim.x;
+      ++it;
       if (t >= x.tiles) {
         nx = item_of(P, it);
         continue;
@@ -413,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float2 l = make_float2(0.f, 0.f), lr = l;
 #pragma unroll 1
       for (int k = 0; k < x.n; ++k) {
-        const int j = x.key_tile(k);
+        const int j = x.key_tile(k, t);
         if (!rr.any(P, j)) continue;
         ok = all_wait(s_full(t), ns & 1, P.err);
         if (!ok) break;
@@ -436,7 +486,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float2 s2 = make_float2(P.scale_log2, P.scale_log2), n2 = make_float2(-m, -m);
           sum = sumr = make_float2(0.f, 0.f);
           auto part = [&](int c, uint32_t (&v)[32]) {
-            if (!whole) {
+            // (a warp's rows cross few of a tile's quarters: 445 cycles for a masked one)
+            if (!whole && __any_sync(0xffffffffu, see[c] != ~0u)) {
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 if (!((see[c] >> e) & 1u)) v[e] = 0xff800000u;
@@ -607,7 +658,8 @@ cudaError_t launch_window_mha(const CUtensorMap& tq, const CUtensorMap& tk, cons
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_smem(window_mha_kernel, static_cast<int>(kSmem), allowed);
   if (e != cudaSuccess) return e;
-  const unsigned grid = static_cast<unsigned>(P.items < a.num_sms ? P.items : a.num_sms);
+  const int grid = P.items < a.num_sms ? P.items : a.num_sms;
+  P.rounds = (P.items + grid - 1) / grid;
   window_mha_kernel<<<grid, kThreads, kSmem, s>>>(tq, tk, tv, P);
   return cudaGetLastError();
 }

@@ -87,6 +87,18 @@ def test_small(lens, lens_q, H, window, sinks):
     check(q, k, v, cu_q, cu_k, out, lse, window, sinks)
 
 
+@pytest.mark.parametrize("window,sinks", [(1, 0), (128, 0), (129, 3), (200, 0), (256, 16), (300, 140)])
+@pytest.mark.parametrize("off", [0, 77, 301])
+def test_ends_of_the_window_of_two_query_tiles(window, sinks, off):
+    """A pair of query tiles shares all key tiles but the window's first and last."""
+    lens_q = [513, 256, 384]
+    lens = [n + off for n in lens_q]
+    q, k, v, cu_q, cu_k, lens_q = make(lens, lens_q, 2, 77 + window + off)
+    out, lse = call(q, k, v, cu_q, cu_k, lens_q, lens, window, sinks)
+    check(q, k, v, cu_q, cu_k, out, lse, window, sinks)
+    assert_no_device_error()
+
+
 @pytest.mark.parametrize("ramp", [(0, 30), (30, 0)])
 def test_references_left_behind(ramp):
     q, k, v, cu_q, cu_k, lens_q = make([640], None, 2, seed=81)
