@@ -260,26 +260,6 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
       : "memory");
 }
 
-// Sums (or maxima) of 16 columns over the lanes of a warp: lanes i and i + 16
-// end with column i's, in 16 shuffles.
-template <bool kMax>
-__device__ __forceinline__ float column_reduce(float (&v)[16]) {
-  const int lane = threadIdx.x % 32;
-#pragma unroll
-  for (int half = 8; half > 0; half >>= 1) {
-    const bool up = (lane & half) != 0;
-#pragma unroll
-    for (int i = 0; i < half; ++i) {
-      const float send = up ? v[i] : v[i + half];
-      const float keep = up ? v[i + half] : v[i];
-      const float got = __shfl_xor_sync(0xffffffffu, send, half);
-      v[i] = kMax ? fmaxf(keep, got) : keep + got;
-    }
-  }
-  const float got = __shfl_xor_sync(0xffffffffu, v[0], 16);
-  return kMax ? fmaxf(v[0], got) : v[0] + got;
-}
-
 // 32 lanes x 32 bits, 16 consecutive columns (thread t <-> lane addr.lane + t).
 __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
