@@ -468,6 +468,9 @@ class _On:
 
     def __init__(self, device, stream):
         import torch
+        on = getattr(stream, "device", None)
+        if on is not None and on.index != device:
+            raise ValueError(f"stream is on {on}, the tensors on cuda:{device}")
         self._ctx = ()
         if device != torch.cuda.current_device():
             self._ctx = (torch.cuda.device(device),)

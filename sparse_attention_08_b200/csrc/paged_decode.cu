@@ -614,6 +614,8 @@ __global__ void __launch_bounds__(128 * kJoin) combine_kernel(Params P) {
   const int per = P.plan[P.c.B];
   const int t0 = P.plan[b];
   const int n = max(seen_of<kTile>(P.c, seq_len(P.c, b)).n, 1);
+  // (after a launch that gave up on a wait the plan may hold anything)
+  if (per < 1 || t0 < 0 || static_cast<int64_t>(t0) + n > static_cast<int64_t>(per) * P.pieces) return;
   const int r0 = t0 / per, r1 = (t0 + n - 1) / per;
   if (r0 == r1) return;
   const int parts = r1 - r0 + 1;

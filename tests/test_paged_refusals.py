@@ -132,3 +132,11 @@ def window_mha(**kw):
 ])
 def test_window_mha_refuses(kw, status):
     assert window_mha(**kw) == status
+
+
+def test_stream_of_another_device_is_refused():
+    class Stream:
+        cuda_stream, device = 0, torch.device("cuda", 1)
+
+    with pytest.raises(ValueError, match="cuda:1"):
+        dsa._On(0, Stream())
