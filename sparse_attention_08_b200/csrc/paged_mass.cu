@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  const Start start = find_start<kTile>(P.c, blockIdx.x, P.pieces, 0, kWarps, scratch, P.err);
+  const Start start = find_start<kTile, false>(P.c, blockIdx.x, P.pieces, 0, kWarps, scratch, P.err);
   tc_fence_after();
   const uint32_t tmem = uniform(*tmem_slot);
   Walk<kTile> w(P.c, start, 0);

@@ -64,6 +64,19 @@ def test_split_over_the_gpu():
     check(c, *run(c))
 
 
+@pytest.mark.parametrize("tiles", [
+    [21] * 41,                              # four whole pieces of five or six tiles each
+    [1 + b % 5 for b in range(120)],        # whole pieces once they may hold a tile more
+    [1 + b % 8 for b in range(128)],        # no whole pieces: cut where the line falls
+    [1 + b % 8 for b in range(129)],        # more sequences than one round takes
+    [40, 0, 90, 3],
+])
+def test_pieces_of_whole_sequences(tiles):
+    lens = [max(0, 64 * n - 7 * b % 60) for b, n in enumerate(tiles)]
+    c = C.Cache(lens, page=32, H=16, seed=len(tiles))
+    check(c, *run(c))
+
+
 def test_many_short_sequences():
     lens = [(37 * i) % 211 for i in range(700)]
     c = C.Cache(lens, page=16, H=16, seed=23)
