@@ -96,12 +96,13 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const Params P) {
   const int rank = C == 1 ? 0 : static_cast<int>(cg::this_cluster().block_rank());
   const int b = blockIdx.x / C;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  grid_wait();
+  grid_release();
   const int n = seq_len(P.c, b);
   const float* row = P.mass + static_cast<int64_t>(b) * P.ld_mass;
   int32_t* idx = P.idx + static_cast<int64_t>(b) * P.budget;
   float* nm = P.new_mass ? P.new_mass + static_cast<int64_t>(b) * P.ld_new : nullptr;
   const int kept = min(n, P.budget);
-  grid_release();
   auto sync_all = [&]() {
     if (C == 1) __syncthreads(); else cg::this_cluster().sync();
   };
@@ -283,6 +284,7 @@ __global__ void __launch_bounds__(256, 4) move_kernel(Params P, uint8_t* pool, i
   const int lane = threadIdx.x % 32;
   const int64_t all = static_cast<int64_t>(groups) * P.c.B;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * 8;
+  grid_release();
   grid_wait();
   for (int64_t t = blockIdx.x * 8ll + threadIdx.x / 32; t < all; t += stride) {
     const int b = static_cast<int>(t / groups);
@@ -331,13 +333,18 @@ cudaError_t launch_select(const Params& P, size_t smem, cudaStream_t s) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = C;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  // (its start under the end of the kernel before: two calls in a row 16.4 -> 15.1 us
+  // for one row of 131072; the attention kernels gain nothing by it, and the decode
+  // lost 4 % where two CTAs read the same keys)
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, select_kernel<C>, P);
 }
 
