@@ -97,6 +97,11 @@ __device__ __forceinline__ bool all_wait(uint32_t bar, uint32_t parity, const De
   return __all_sync(0xffffffffu, ok);
 }
 
+// The same by one lane alone, inside the branch that issues MMAs.
+__device__ __forceinline__ bool one_wait(uint32_t bar, uint32_t parity, const DevErr& e) {
+  return mbar_try_wait(bar, parity) || wait_loop(bar, parity, e.word, e.gen, e.limit_ns);
+}
+
 // A value that all lanes hold alike, in a form the compiler knows to be so: MMA
 // operands made from it stay in uniform registers.
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }

@@ -35,9 +35,9 @@
 // waits behind the other.
 //
 // What bounds it, on 64 sequences of 4K-128K: with up to 64 heads the cache's one
-// read (16 heads 790 us, 6.4 TB/s; 64 heads 893 us, 5.7 TB/s); with 128 the tensor
+// read (16 heads 780 us, 6.5 TB/s; 64 heads 876 us, 5.8 TB/s); with 128 the tensor
 // cores, whose products take 2600 cycles a tile as issued (S^T 1650, M = 64 at 46
-// cycles each; O^T 950): 1.52 ms, 800 TFLOP/s.  One tile of 128 keys at a time (M =
+// cycles each; O^T 950): 1.50 ms, 815 TFLOP/s.  One tile of 128 keys at a time (M =
 // 128 for S^T) needs only 3300 tensor cycles per 128 keys, but idles through its
 // softmax and reload: 5900 cycles in all, 1.54 ms with 128 heads and 967 us with 64.
 //
@@ -267,32 +267,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t d = tmem + kColS + (slot << 20);           // lane offset 16 for slot 1
         // (the slot's last scores have been read: its latents could only be
         // replaced after the product that their weights went into)
-#pragma unroll
-        for (int c = 0; c < 8; c += 4) {
-          ok = ok && all_wait(full(slot, c / 2), ph, P.err);
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) {
+        ok = ok && all_wait(full(slot, 0), ph, P.err);
+        if (!ok) break;
+        tc_fence_after();
+        // The issuing lane waits for the other parts alone: with a wait and a vote of
+        // the warp between the runs 64 sequences of 4K-128K took 1548 us (128 heads;
+        // 64: 900, 16: 800), so 1499 (876, 784).
+        bool lost = false;
+        if (elect_one()) {
+          auto run = [&](int c) {
 #pragma unroll
             for (int kk = 0; kk < 16; ++kk)
               mma_f16(d, a + (((c + kk / 4) * kChunkBytes + (kk % 4) * 32) >> 4),
                       dQ + (((c + kk / 4) * kQChunk + (kk % 4) * 32) >> 4), kIdescS,
                       c + kk > 0 ? 1u : 0u);
-          }
-          __syncwarp();
-        }
-        ok = ok && all_wait(full(slot, 4), ph, P.err);
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
+          };
+          run(0);
+          lost = !one_wait(full(slot, 2), ph, P.err);
+          tc_fence_after();
+          if (!lost) run(4);
+          lost = lost || !one_wait(full(slot, 4), ph, P.err);
+          tc_fence_after();
+          if (!lost)
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_f16(d, a + ((8 * kChunkBytes + kk * 32) >> 4), dQ + ((8 * kQChunk + kk * 32) >> 4),
-                    kIdescS, 1u);
+            for (int kk = 0; kk < 4; ++kk)
+              mma_f16(d, a + ((8 * kChunkBytes + kk * 32) >> 4), dQ + ((8 * kQChunk + kk * 32) >> 4),
+                      kIdescS, 1u);
           mma_commit(s_full(slot));
           if (i + 1 == w.i1) mma_commit(q_empty);
         }
-        __syncwarp();
+        ok = !__any_sync(0xffffffffu, lost);
       }
     }
     mma_commit_warp(drain);

@@ -338,9 +338,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t v0 = box, k0 = box + (i >= 0 ? 2 + vs : 0);
         const uint32_t vb = uniform(v0 + vs * t), kb = uniform(k0 + ks * t);
         // Values and the turn first: the weights then meet an issuer with no other wait
-        // left (each one costs it 200 cycles, there or not).  The next keys after the
-        // product: they come half a step later, when the other query tile has let go of
-        // the boxes (waited for first: causal 654 against 622 us).
+        // left (each one costs it 200 cycles, there or not; the weights before the turn:
+        // causal 653 against 640 us).  The next keys after the product: they come
+        // half a step later, when the other query tile has let go of the boxes (waited for
+        // first: 654 against 622).  The issuing lane waits for them alone (640 -> 630; all
+        // waits by that lane: 688).
         if (i >= 0) {
           ok = all_wait(full(unit), (unit / 4) & 1, P.err);
           if (!ok) break;
@@ -370,6 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++ns;
         }
         tc_fence_after();
+        bool lost = false;
         if (elect_one()) {
           if (pv) {
             const uint64_t b0 = dV + (((vb & (kRing - 1)) * kBox) >> 4);
@@ -390,16 +393,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_commit(empty(vb));
             mma_commit(empty(vb + 1));
           }
-        }
-        __syncwarp();
-        if (i + 1 < x.n) {
-          ok = all_wait(full(unit), (unit / 4) & 1, P.err);
-          if (!ok) break;
-          ++unit;
-        }
-        tc_fence_after();
-        if (elect_one()) {
-          if (sn) {
+          bool there = true;
+          if (i + 1 < x.n) {
+            there = paged::one_wait(full(unit), (unit / 4) & 1, P.err);
+            tc_fence_after();
+          }
+          lost = !there;
+          if (sn && there) {
 #pragma unroll
             for (int c = 0; c < 3; ++c) {
               const uint64_t b = dR + ((((kb + c) & (kRing - 1)) * kBox) >> 4);
@@ -416,6 +416,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         __syncwarp();
+        if (i + 1 < x.n) {
+          ++unit;
+          ok = !__any_sync(0xffffffffu, lost);
+          if (!ok) break;
+        }
         if (pv) more = 1;
         // boxes that this query tile has no use for
         if (i >= 0 && !pv && lane < 2) mbar_arrive(empty(vb + lane));
