@@ -745,7 +745,11 @@ cudaError_t launch_paged_decode(const CUtensorMap& tq, const CUtensorMap& tx,
   // With few sequences each is cut into many parts, which four thread groups
   // share (one of 131072 entries, 74 parts: 29 -> 13 us); with many, a sequence
   // has two or three and the larger CTAs only cost (48 sequences: 10 against 20 us).
+  // Eight groups where every CTA has an SM to itself (one sequence, both kernels: 16
+  // heads 53.2 -> 50.9 us, 128 heads 69.4 -> 68.2; 16 sequences of 64 heads 45 -> 55).
   const dim3 grid(static_cast<unsigned>(a.H), y, z);
+  if (static_cast<int64_t>(a.cache.B) * a.H <= kMaxCtas)
+    return launch_after(combine_kernel<8>, grid, 1024, 0, s, P);
   return a.cache.B * 4 < P.pieces ? launch_after(combine_kernel<4>, grid, 512, 0, s, P)
                                   : launch_after(combine_kernel<1>, grid, 128, 0, s, P);
 }

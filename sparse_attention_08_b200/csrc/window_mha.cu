@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && lane == 0) {
       if (nq0 > 0) mbar_wait_drain(q_full(0), (nq0 - 1) & 1, P.err);
       if (nq1 > 0) mbar_wait_drain(q_full(1), (nq1 - 1) & 1, P.err);
-      for (uint32_t u = unit > 2 ? unit - 2 : 0; u <= unit; ++u)
+      for (uint32_t u = unit > 3 ? unit - 3 : 0; u <= unit; ++u)
         if (u < unit || box > 0) mbar_wait_drain(full(u), (u / 4) & 1, P.err);
     }
     __syncwarp();

@@ -65,6 +65,7 @@ def test_split_over_the_gpu():
 
 
 @pytest.mark.parametrize("tiles", [
+    [9] * 20,                               # (the join in four groups of threads)
     [21] * 41,                              # four whole pieces of five or six tiles each
     [1 + b % 5 for b in range(120)],        # whole pieces once they may hold a tile more
     [1 + b % 8 for b in range(128)],        # no whole pieces: cut where the line falls
