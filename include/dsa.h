@@ -42,8 +42,11 @@
  *
  *  Errors: each call validates its arguments before launching anything and
  *  returns a status; CUDA launch errors map to DSA_ERR_CUDA.  Kernels bound
- *  every wait; a wait that runs out sets a device error word and the kernel
- *  returns early.  dsa_get_device_error() reads and clears that word.
+ *  every wait; a wait that runs out sets a device error word and that launch
+ *  returns early.  An input error found on the device (DSA_ERR_BOUNDS) is
+ *  reported in the same word and ends nothing.  Neither touches other launches,
+ *  replays of captured ones among them.  dsa_get_device_error() reads and
+ *  clears the word.
  */
 #ifndef DSA_H_
 #define DSA_H_

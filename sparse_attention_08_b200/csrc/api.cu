@@ -18,7 +18,7 @@
 
 namespace {
 
-__device__ unsigned g_dsa_err[2];  // [0] sticky error bits, [1] newest failed launch generation
+__device__ unsigned g_dsa_err[2];  // [0] sticky error bits, [1] generation of the launch that last timed out
 
 std::atomic<unsigned> g_generation{1};
 
@@ -67,7 +67,9 @@ dsa_status_t device_info(DeviceInfo** out) {
 dsa::DevErr next_err(const DeviceInfo* d) {
   dsa::DevErr e;
   e.word = d->err;
-  e.gen = g_generation.fetch_add(1);
+  do {
+    e.gen = g_generation.fetch_add(1);
+  } while (e.gen == 0);                // (wrapped around: 0 is a cleared word)
   e.inject = 0;
   const uint64_t lim = g_wait_limit_ns.load();
   e.limit_ns = lim != 0 ? lim : dsa::kWaitLimitNs;
@@ -916,8 +918,8 @@ dsa_status_t dsa_get_device_error(void* stream) {
   unsigned bits = 0;
   if (cudaMemcpyFromSymbol(&bits, g_dsa_err, sizeof(unsigned)) != cudaSuccess) return DSA_ERR_CUDA;
   if (bits == 0) return DSA_OK;
-  const unsigned zero = 0;
-  if (cudaMemcpyToSymbol(g_dsa_err, &zero, sizeof(unsigned)) != cudaSuccess) return DSA_ERR_CUDA;
+  const unsigned zero[2] = {0, 0};
+  if (cudaMemcpyToSymbol(g_dsa_err, zero, sizeof(zero)) != cudaSuccess) return DSA_ERR_CUDA;
   if (bits & dsa::kErrTimeout) return DSA_ERR_TIMEOUT;
   return DSA_ERR_BOUNDS;
 }

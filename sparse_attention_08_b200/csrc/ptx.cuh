@@ -17,10 +17,12 @@ namespace dsa {
 // ---------------------------------------------------------------------------
 // Device error reporting.
 // ---------------------------------------------------------------------------
-// err[0]: sticky error bits read (and cleared) by dsa_get_device_error();
-// err[1]: generation of the newest launch that failed.  Each launch carries
-// its own generation number; a wait gives up early once its own launch has
-// failed elsewhere, so one timeout does not cost a timeout per CTA.
+// err[0]: sticky error bits, err[1]: generation of the launch that last timed
+// out; dsa_get_device_error() reads the bits and clears both.  Each launch
+// carries its own generation number (never 0; a captured one the same in every
+// replay), and a wait gives up early once that very launch has timed out elsewhere, so
+// one timeout does not cost a timeout per CTA.  An input error (kErrBounds) is only
+// reported: its launch, and every other, goes on.
 enum : unsigned {
   kErrTimeout = 1u,
   kErrBounds = 2u,
@@ -48,11 +50,11 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 
 __device__ __forceinline__ void raise_error(const DevErr& e, unsigned bits) {
   atomicOr(e.word, bits);
-  atomicMax(e.word + 1, e.gen);
+  if (bits & kErrTimeout) atomicExch(e.word + 1, e.gen);
 }
 
 __device__ __forceinline__ bool launch_failed(const DevErr& e) {
-  return *reinterpret_cast<volatile unsigned*>(e.word + 1) >= e.gen;
+  return *reinterpret_cast<volatile unsigned*>(e.word + 1) == e.gen;
 }
 
 // Longest a single wait may take before the kernel declares a timeout,
