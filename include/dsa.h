@@ -575,7 +575,9 @@ DSA_API dsa_status_t dsa_get_device_error(void* stream);
  *  - drop_first_key_load != 0: the NEXT dsa_indexer_logits launch (only that
  *    one) leaves out the first key-tile load of every CTA, so the MMA
  *    issuer's wait for that tile runs out; that launch's scores are then
- *    incomplete and dsa_get_device_error() returns DSA_ERR_TIMEOUT.
+ *    incomplete and dsa_get_device_error() returns DSA_ERR_TIMEOUT.  If the next
+ *    of these launches is dsa_paged_mla_decode's, dsa_paged_attn_mass's or
+ *    dsa_window_mha_fwd's, it loads half the rows of its key boxes, to the same end.
  * Process-wide host state, not thread-safe against concurrent launches.
  */
 DSA_API void dsa_debug_fault_injection(uint64_t wait_limit_ns, int drop_first_key_load);

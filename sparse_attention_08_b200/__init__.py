@@ -125,8 +125,9 @@ def load():
 
 def dsa_debug_fault_injection(wait_limit_ns: int = 0, drop_first_key_load: bool = False):
     """Test hook: the wait limit of later launches (0 = the default 2 s) and a
-    one-shot request that the next dsa_indexer_logits launch leave out its
-    first key-tile load, so a bounded wait runs out (DSA_ERR_TIMEOUT)."""
+    one-shot request that the next launch of dsa_indexer_logits (or of the paged
+    decode and totals, or of the windowed prompt attention) leave out keys that it
+    waits for, so a bounded wait runs out (DSA_ERR_TIMEOUT)."""
     load().dsa_debug_fault_injection(int(wait_limit_ns), 1 if drop_first_key_load else 0)
 
 

@@ -23,9 +23,9 @@ __device__ unsigned g_dsa_err[2];  // [0] sticky error bits, [1] generation of t
 std::atomic<unsigned> g_generation{1};
 
 // Test hook state (dsa_debug_fault_injection): the wait limit of later
-// launches (0 = the default) and a one-shot request for the indexer.
+// launches (0 = the default) and a one-shot request to lose a load.
 std::atomic<uint64_t> g_wait_limit_ns{0};
-std::atomic<unsigned> g_inject_indexer{0};
+std::atomic<unsigned> g_inject{0};
 
 constexpr int kMaxDevices = 64;
 struct DeviceInfo {
@@ -62,6 +62,12 @@ dsa_status_t device_info(DeviceInfo** out) {
   }
   *out = &d;
   return DSA_OK;
+}
+
+// The test hook for the kernels that load keys as TMA boxes: half of a box's rows,
+// so that what is waited for never comes whole.
+int rows_loaded(int box_rows) {
+  return g_inject.exchange(0) & dsa::kInjectDropFirstKeyLoad ? box_rows / 2 : box_rows;
 }
 
 dsa::DevErr next_err(const DeviceInfo* d) {
@@ -207,7 +213,7 @@ dsa_status_t dsa_indexer_logits(const void* q_fp8, const float* q_scale, const f
   a.ld = ld_logits;
   a.tile_n = tile_n;
   dsa::DevErr err = next_err(dev);
-  err.inject = g_inject_indexer.exchange(0);
+  err.inject = g_inject.exchange(0);
   return from_cuda(dsa::launch_indexer(tq, tk, a, dev->num_sms, err,
                                        static_cast<cudaStream_t>(stream)));
 }
@@ -362,7 +368,7 @@ dsa_status_t dsa_window_mha_fwd(const void* q, const void* k, const void* v,
   if ((st = device_info(&dev)) != DSA_OK) return st;
   CUtensorMap tq, tk, tv;
   if ((st = encode_3d_bf16(&tq, q, 192, H, total_q, 64, 128)) != DSA_OK) return st;
-  if ((st = encode_3d_bf16(&tk, k, 192, H, total_k, 64, 128)) != DSA_OK) return st;
+  if ((st = encode_3d_bf16(&tk, k, 192, H, total_k, 64, rows_loaded(128))) != DSA_OK) return st;
   if ((st = encode_3d_bf16(&tv, v, 128, H, total_k, 64, 128)) != DSA_OK) return st;
   dsa::WindowMhaArgs a;
   a.cu_q = cu_seqlens_q;
@@ -810,7 +816,8 @@ dsa_status_t dsa_paged_mla_decode(const void* q, const void* kv_cache, int64_t n
                       2, H < 64 ? static_cast<uint32_t>(H) : 64u, 64,
                       CU_TENSOR_MAP_SWIZZLE_128B)) != DSA_OK)
     return st;
-  if ((st = encode_pool(&tx, kv_cache, n_pages, page_size, page_stride, a.cache.box)) != DSA_OK)
+  if ((st = encode_pool(&tx, kv_cache, n_pages, page_size, page_stride,
+                        rows_loaded(a.cache.box))) != DSA_OK)
     return st;
   return from_cuda(
       dsa::launch_paged_decode(tq, tx, a, next_err(dev), static_cast<cudaStream_t>(stream)));
@@ -856,7 +863,8 @@ dsa_status_t dsa_paged_attn_mass(const void* q, const void* kv_cache, int64_t n_
       return st;
     err[i] = next_err(dev);
   }
-  if ((st = encode_pool(&tx, kv_cache, n_pages, page_size, page_stride, a.cache.box)) != DSA_OK)
+  if ((st = encode_pool(&tx, kv_cache, n_pages, page_size, page_stride,
+                        rows_loaded(a.cache.box))) != DSA_OK)
     return st;
   return from_cuda(
       dsa::launch_paged_mass(tq, launches, tx, a, err, static_cast<cudaStream_t>(stream)));
@@ -907,7 +915,7 @@ dsa_status_t dsa_cache_evict(void* kv_cache, int64_t n_pages, int page_size, int
 
 void dsa_debug_fault_injection(uint64_t wait_limit_ns, int drop_first_key_load) {
   g_wait_limit_ns.store(wait_limit_ns);
-  g_inject_indexer.store(drop_first_key_load ? dsa::kInjectDropFirstKeyLoad : 0u);
+  g_inject.store(drop_first_key_load ? dsa::kInjectDropFirstKeyLoad : 0u);
 }
 
 dsa_status_t dsa_get_device_error(void* stream) {

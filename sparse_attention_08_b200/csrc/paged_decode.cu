@@ -224,8 +224,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
     }
-    // after a failure, let the copies in flight land before the memory goes
-    if (!ok && lane == 0) {
+    // Let the copies in flight land before the memory goes: this warp may have asked
+    // for its last tile when the ones that wait for it give up.
+    if (lane == 0) {
 #pragma unroll 1
       for (uint32_t u = 0; u < 2; ++u)
 #pragma unroll 1

@@ -152,9 +152,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         x = nx;
       }
     }
-    // after a failure, let the copies in flight land before the memory goes:
-    // every stage's newest phase completes, or the wait's limit passes
-    if (!ok && lane == 0) {
+    // Let the copies in flight land before the memory goes (these warps may have
+    // asked for their last chunk when the ones that wait for it give up): every stage's
+    // newest phase completes, or the wait's limit passes.
+    if (lane == 0) {
       if (warp == 0 && seg > 0) mbar_wait_drain(q_full, (seg - 1) & 1, P.err);
 #pragma unroll 1
       for (uint32_t u = t > static_cast<uint32_t>(P.stages) ? t - P.stages : 0; u < t; ++u)

@@ -280,12 +280,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         load(&tv, 2, x.h, row, second);
       }
     }
-    // after a failure, let the copies in flight land before the memory goes
-    if (!ok && lane == 0) {
+    // Let the copies in flight land before the memory goes: this warp may have asked
+    // for its last unit when the ones that wait for it give up.  (After a failure of
+    // its own, a unit may also have been asked for in part.)
+    if (lane == 0) {
       if (nq0 > 0) mbar_wait_drain(q_full(0), (nq0 - 1) & 1, P.err);
       if (nq1 > 0) mbar_wait_drain(q_full(1), (nq1 - 1) & 1, P.err);
       for (uint32_t u = unit > 3 ? unit - 3 : 0; u <= unit; ++u)
-        if (u < unit || box > 0) mbar_wait_drain(full(u), (u / 4) & 1, P.err);
+        if (u < unit || (!ok && box > 0)) mbar_wait_drain(full(u), (u / 4) & 1, P.err);
     }
     __syncwarp();
   } else if (warp < 3) {

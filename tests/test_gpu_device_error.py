@@ -4,6 +4,8 @@ A captured launch keeps its number in every replay, so a later launch's report m
 not make its waits give up.  That is made visible with the library's test hook: a
 captured indexer launch leaves out its first key-tile load, and has to say so itself
 (DSA_ERR_TIMEOUT) after its own wait limit of 20 ms, whatever was reported before."""
+import time
+
 import pytest
 import torch
 
@@ -80,3 +82,50 @@ def test_a_bad_page_reads_as_zeros_and_the_rest_is_computed():
         assert dsa.dsa_get_device_error() == (DSA_ERR_BOUNDS if i else 0)
     for x in (o, l, m):
         assert torch.isfinite(x.float()).all() and torch.equal(x[0], x[1])
+
+
+def calls():
+    """The kernels with roles that wait for one another: name, call and outputs."""
+    c = P.Cache([5000, 70, 3000, 64, 1], page=64, H=64, seed=34)
+    pool, table, n, q = c.to_gpu()
+    ws = torch.zeros(dsa.dsa_paged_mla_decode_workspace_size(c.B, 64, c.max_len), dtype=torch.uint8,
+                     device="cuda")
+    o, l = torch.empty((c.B, 64, 512), dtype=torch.bfloat16, device="cuda"), torch.empty((c.B, 64), device="cuda")
+    m = torch.zeros((c.B, c.max_len), device="cuda")
+    g = torch.Generator().manual_seed(35)
+    cu = torch.tensor([0, 600, 610, 1010], dtype=torch.int32, device="cuda")
+    x = [torch.randn((1010, 16, d), generator=g).to(torch.bfloat16).cuda() for d in (192, 192, 128)]
+    wo, wl = torch.empty_like(x[2]), torch.empty((1010, 16), device="cuda")
+    return [
+        ("decode", lambda: dsa.dsa_paged_mla_decode(q, pool, table, n, c.max_len, P.SCALE, o, l, workspace=ws),
+         [o, l]),
+        ("mass", lambda: dsa.dsa_paged_attn_mass(q, pool, table, n, l, c.max_len, P.SCALE, m), [m]),
+        ("window", lambda: dsa.dsa_window_mha_fwd(*x, cu, cu, 3, 600, 600, 200, 4, 0.07, wo, wl), [wo, wl]),
+    ]
+
+
+@pytest.mark.parametrize("which", [0, 1, 2], ids=["decode", "mass", "window"])
+def test_a_timed_out_wait_is_reported_and_the_next_call_has_the_same_bits(which):
+    todo = calls()
+    todo[0][1]()
+    name, call, outs = todo[which]
+    call()
+    C.assert_no_device_error()
+    want = [t.clone() for t in outs]
+    dsa.dsa_debug_fault_injection(20_000_000, True)
+    try:
+        t0 = time.perf_counter()
+        call()
+        torch.cuda.synchronize()
+        took = time.perf_counter() - t0
+        assert dsa.dsa_get_device_error() == DSA_ERR_TIMEOUT, name
+    finally:
+        dsa.dsa_debug_fault_injection(0, False)
+    # a dozen limits of 20 ms one after the other, not the default 2 s
+    assert took < 1.5, took
+    if which:
+        todo[0][1]()
+    call()
+    C.assert_no_device_error()
+    for a, b in zip(outs, want):
+        assert torch.equal(a, b), name
