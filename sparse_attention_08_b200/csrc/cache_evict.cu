@@ -98,7 +98,11 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const Params P) {
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   grid_wait();
   grid_release();
-  const int n = seq_len(P.c, b);
+  // Lengths and totals by plain loads: the kernel before on the stream may have written
+  // them while this one was already here, which a load through the read-only path
+  // (__ldg) would rule out, and only plain ones are kept behind the wait.
+  const int raw = P.c.lens[b];
+  const int n = min(max(raw, 0), P.c.cap);
   const float* row = P.mass + static_cast<int64_t>(b) * P.ld_mass;
   int32_t* idx = P.idx + static_cast<int64_t>(b) * P.budget;
   float* nm = P.new_mass ? P.new_mass + static_cast<int64_t>(b) * P.ld_new : nullptr;
@@ -111,7 +115,6 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const Params P) {
   };
   if (rank == 0 && tid == 0) {
     P.new_lens[b] = kept;
-    const int raw = __ldg(P.c.lens + b);
     if (raw < 0 || raw > P.c.cap) raise_error(P.err, kErrBounds);
   }
   const bool cut = n > P.budget;
@@ -122,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const Params P) {
     if (j >= head && j < tail) continue;
     const int s = j < head ? j : (cut ? n - P.budget + j : -1);
     idx[j] = s;
-    if (nm) nm[j] = s >= 0 ? __ldg(row + s) : 0.f;
+    if (nm) nm[j] = s >= 0 ? row[s] : 0.f;
   }
   const int room = P.budget - P.sinks - P.recent;
   if (!cut || room <= 0) return;         // the whole cluster alike
@@ -140,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const Params P) {
   for (int i = lane; i < len; i += 32 * kAhead) {
     float x[kAhead];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) x[u] = i + 32 * u < len ? __ldg(src + i + 32 * u) : 0.f;
+    for (int u = 0; u < kAhead; ++u) x[u] = i + 32 * u < len ? src[i + 32 * u] : 0.f;
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       if (i + 32 * u < len) {
@@ -269,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const Params P) {
       // the total itself, from its key unless that stands for several
       if (nm) {
         const uint32_t k = mine[slot_of(i0 + u)];
-        nm[j] = k == 0xFFFFFFFFu || k == 0x80000000u ? __ldg(row + s) : key_value(k);
+        nm[j] = k == 0xFFFFFFFFu || k == 0x80000000u ? row[s] : key_value(k);
       }
     }
     if (over) ++bg; else ++be;
@@ -284,6 +287,7 @@ __global__ void __launch_bounds__(256, 4) move_kernel(Params P, uint8_t* pool, i
   const int lane = threadIdx.x % 32;
   const int64_t all = static_cast<int64_t>(groups) * P.c.B;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * 8;
+  // (the tables are not written under this kernel: it starts when the choice has passed its own wait)
   grid_release();
   grid_wait();
   for (int64_t t = blockIdx.x * 8ll + threadIdx.x / 32; t < all; t += stride) {

@@ -148,3 +148,59 @@ def test_replayed_in_a_graph_follows_the_lengths():
             keep = keep_of(m[b], n, 64, 4, 8)
             assert idx[b].cpu().tolist() == keep + [-1] * (64 - len(keep))
             assert int(nl[b]) == len(keep)
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_cuts_of_cuts_without_a_pause(graph):
+    """Each cut reads the lengths, totals, table and latents that the one before it on the
+    stream has only just written (or is still writing when it starts)."""
+    lens, page, budgets = [30000, 9000, 2500, 31000], 64, [9000, 4000, 900]
+    c = C.Cache(lens, page=page, H=16, seed=72, extra_pages=sum(pages_for(lens, k, page) for k in budgets))
+    m = totals(c, 73, "zeros")
+    tables, at = [], 0
+    for k in budgets:
+        t = torch.full((4, -(-k // page)), -1, dtype=torch.int32)
+        for b, n in enumerate(lens):
+            need = -(-min(n, k) // page)
+            t[b, :need] = c.free_pages[at:at + need]
+            at += need
+        tables.append(t)
+    pool, table, n_d, _ = c.to_gpu()
+    first = pool.clone()
+    dev = [t.cuda() for t in tables]
+    idx = [torch.empty((4, k), dtype=torch.int32, device="cuda") for k in budgets]
+    n_new = [torch.empty_like(n_d) for _ in budgets]
+    m_new = [torch.empty((4, k), device="cuda") for k in budgets]
+    m_d = m.cuda()
+
+    def cuts():
+        tab, n, mass, most = table, n_d, m_d, c.max_len
+        for i, k in enumerate(budgets):
+            dsa.dsa_cache_evict(pool, tab, n, mass, most, k, 4, 100, dev[i], n_new[i], idx[i], m_new[i])
+            tab, n, mass, most = dev[i], n_new[i], m_new[i], k
+
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            cuts()
+        g.replay()
+        g.replay()
+    else:
+        cuts()
+    assert_no_device_error()
+    assert torch.equal(table, c.table.cuda())
+    for b, n in enumerate(lens):
+        row, rows, held = m[b], c.rows(b), n
+        for i, k in enumerate(budgets):
+            keep = keep_of(row, held, k, 4, 100)
+            held = len(keep)
+            assert int(n_new[i][b]) == held
+            assert idx[i][b].cpu().tolist() == keep + [-1] * (k - held)
+            row, rows = torch.cat([row[keep], torch.zeros(k - held)]), rows[keep]
+            assert torch.equal(m_new[i][b].cpu().view(torch.int32), row.view(torch.int32))
+            got = pool[tables[i][b, :-(-held // page)].long().cuda()].reshape(-1, 576)[:held].cpu()
+            assert torch.equal(got.view(torch.int16), rows.view(torch.int16))
+    used = torch.cat([t[t >= 0] for t in tables]).long()
+    rest = torch.ones(c.n_pages, dtype=torch.bool)
+    rest[used] = False
+    assert torch.equal(pool[rest.cuda()].view(torch.int16), first[rest.cuda()].view(torch.int16))
