@@ -442,6 +442,8 @@ DSA_API dsa_status_t dsa_window_mha_fwd(const void* q, const void* k, const void
  *           own among them; 0 is allowed.  Rows of a page behind the length
  *           are never used, whatever they hold.
  *  max_len_k bounds the lengths (at most 2^24).
+ *  An array without an element (B = 0, or one value per entry and max_len_k = 0)
+ *  may be NULL; so may dsa_window_mha_fwd's of total_q = 0.
  *
  * A length outside [0, min(max_len_k, max_pages * page_size)] is cut to that
  * range, and a page id outside the pool reads as rows of zeros; both set

@@ -354,7 +354,9 @@ dsa_status_t dsa_window_mha_fwd(const void* q, const void* k, const void* v,
   dsa_status_t st = check_varlen(cu_seqlens_q, cu_seqlens_k, B, max_len_q, max_len_k, total_q,
                                  total_k);
   if (st != DSA_OK) return st;
-  if (!q || !k || !v || !out || window < 0 || sinks < 0) return DSA_ERR_INVALID_ARG;
+  if (window < 0 || sinks < 0) return DSA_ERR_INVALID_ARG;
+  // (an empty tensor's address may be null)
+  if (total_q > 0 && (!q || !k || !v || !out)) return DSA_ERR_INVALID_ARG;
   if (d_qk != 192 || d_v != 128 || H < 1 || H > 65535 || max_len_k > (1 << 24))
     return DSA_ERR_UNSUPPORTED;
   if (!(sm_scale > 0.f) || sm_scale != sm_scale) return DSA_ERR_INVALID_ARG;
@@ -734,12 +736,15 @@ dsa_status_t dsa_forward_fused(const void* q_fp8, const float* q_scale, const fl
 
 namespace {
 
-// The arguments that every call over a paged cache takes.
+// The arguments that every call over a paged cache takes.  (An empty tensor's address
+// may be null: here and in the calls, what has one value per sequence is needed for B > 0,
+// what has one per entry for max_len_k > 0 too.)
 dsa_status_t check_cache(const void* kv_cache, int64_t n_pages, int page_size,
                          int64_t page_stride, const int32_t* block_table, int64_t block_table_ld,
                          int max_pages, const int32_t* seq_lens, int B, int max_len_k) {
-  if (!kv_cache || !block_table || !seq_lens || B < 0 || max_len_k < 0 || n_pages < 1 ||
-      page_size < 1 || max_pages < 1 || block_table_ld < max_pages)
+  if (B > 0 && (!block_table || !seq_lens)) return DSA_ERR_INVALID_ARG;
+  if (!kv_cache || B < 0 || max_len_k < 0 || n_pages < 1 || page_size < 1 || max_pages < 1 ||
+      block_table_ld < max_pages)
     return DSA_ERR_INVALID_ARG;
   if (page_size % 16 != 0 || page_size > 65536 || n_pages >= (int64_t(1) << 31) ||
       max_len_k > (1 << 24))
@@ -788,7 +793,7 @@ dsa_status_t dsa_paged_mla_decode(const void* q, const void* kv_cache, int64_t n
                                   const int32_t* seq_lens, int B, int max_len_k, int H, int d_qk, int d_v, int window, int sinks,
                                   float sm_scale, void* out, float* lse, void* workspace,
                                   size_t workspace_bytes, void* stream) {
-  if (!q || !out || window < 0 || sinks < 0) return DSA_ERR_INVALID_ARG;
+  if ((B > 0 && (!q || !out)) || window < 0 || sinks < 0) return DSA_ERR_INVALID_ARG;
   if (d_qk != 576 || d_v != 512 || !mla_heads_ok(H)) return DSA_ERR_UNSUPPORTED;
   dsa_status_t st = check_cache(kv_cache, n_pages, page_size, page_stride, block_table,
                                 block_table_ld, max_pages, seq_lens, B, max_len_k);
@@ -829,7 +834,8 @@ dsa_status_t dsa_paged_attn_mass(const void* q, const void* kv_cache, int64_t n_
                                  int B, int max_len_k, int H, int d_qk, int window, int sinks,
                                  float sm_scale, const float* lse, const float* mass_in,
                                  float* mass_out, int64_t ld_mass, void* stream) {
-  if (!q || !lse || !mass_out || window < 0 || sinks < 0) return DSA_ERR_INVALID_ARG;
+  if ((B > 0 && (!q || !lse || (max_len_k > 0 && !mass_out))) || window < 0 || sinks < 0)
+    return DSA_ERR_INVALID_ARG;
   if (d_qk != 576 || !mla_heads_ok(H)) return DSA_ERR_UNSUPPORTED;
   dsa_status_t st = check_cache(kv_cache, n_pages, page_size, page_stride, block_table,
                                 block_table_ld, max_pages, seq_lens, B, max_len_k);
@@ -877,15 +883,17 @@ dsa_status_t dsa_cache_evict(void* kv_cache, int64_t n_pages, int page_size, int
                              const int32_t* new_block_table, int64_t new_block_table_ld,
                              int new_max_pages, int32_t* new_lens, int32_t* idx_out,
                              float* new_mass, int64_t ld_new_mass, void* stream) {
-  if (!mass || !new_block_table || !new_lens || !idx_out || budget < 1 || sinks < 0 || recent < 0)
+  if (B > 0 && (!new_block_table || !new_lens || !idx_out || (max_len_k > 0 && !mass)))
     return DSA_ERR_INVALID_ARG;
+  if (budget < 1 || sinks < 0 || recent < 0) return DSA_ERR_INVALID_ARG;
   dsa_status_t st = check_cache(kv_cache, n_pages, page_size, page_stride, block_table,
                                 block_table_ld, max_pages, seq_lens, B, max_len_k);
   if (st != DSA_OK) return st;
   if (max_len_k > 262144) return DSA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(sinks) + recent > budget) return DSA_ERR_INVALID_ARG;
   if (ld_mass < max_len_k || (new_mass && ld_new_mass < budget)) return DSA_ERR_INVALID_ARG;
-  if (new_lens == seq_lens || new_mass == mass) return DSA_ERR_INVALID_ARG;
+  if ((new_lens && new_lens == seq_lens) || (new_mass && new_mass == mass))
+    return DSA_ERR_INVALID_ARG;
   const int64_t most = budget < max_len_k ? budget : max_len_k;
   if (new_max_pages < 1 || new_block_table_ld < new_max_pages ||
       static_cast<int64_t>(new_max_pages) * page_size < most)

@@ -156,3 +156,26 @@ def test_serving_steps():
         n = held[b].shape[0]
         assert n == budget + steps
         assert float((new_mass[b, :n].cpu().double() - total[b][:n]).abs().max()) < 1e-4 * 2 * steps * H
+
+
+def test_empty_batches():
+    """No sequences, or sequences without room for an entry: the addresses of empty tensors are
+    null, and nothing is to be read or written through them."""
+    dev, bf16, i32 = "cuda", torch.bfloat16, torch.int32
+    pool = torch.full((3, PAGE, 576), float("nan"), dtype=bf16, device=dev)
+    for B, most in ((0, 40), (0, 0), (2, 0)):
+        q = torch.ones((B, H, 576), dtype=bf16, device=dev)
+        table = torch.full((B, 3), -1, dtype=i32, device=dev)
+        n = torch.zeros(B, dtype=i32, device=dev)
+        out = torch.full((B, H, 512), 7.0, dtype=bf16, device=dev)
+        lse = torch.full((B, H), 7.0, device=dev)
+        mass = torch.empty((B, most), device=dev)
+        new_mass = torch.full((B, 20), 7.0, device=dev)
+        new_n, idx = torch.full_like(n, 7), torch.full((B, 20), 7, dtype=i32, device=dev)
+        dsa.dsa_paged_mla_decode(q, pool, table, n, most, 0.04, out, lse)
+        dsa.dsa_paged_attn_mass(q, pool, table, n, lse, most, 0.04, mass, mass_in=mass)
+        dsa.dsa_cache_evict(pool, table, n, mass, most, 20, 2, 4, table + 1, new_n, idx, new_mass)
+        assert_no_device_error()
+        assert (out == 0).all() and torch.isneginf(lse).all()
+        assert (new_n == 0).all() and (idx == -1).all() and (new_mass == 0).all()
+    assert torch.isnan(pool.float()).all()

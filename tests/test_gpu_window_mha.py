@@ -203,3 +203,13 @@ def test_more_queries_than_keys_is_reported():
     assert dsa.dsa_get_device_error() == DSA_ERR_BOUNDS
     assert (out[:40] == 7).all()
     check(q, k, v, cu_q, cu_k, out, None, 8, 1, seqs=[1])
+
+
+def test_no_queries():
+    """Nothing to do, with the null addresses that empty tensors have."""
+    cu = torch.zeros(3, dtype=torch.int32, device="cuda")
+    e = lambda d: torch.empty((0, 2, d), dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    dsa.dsa_window_mha_fwd(e(192), e(192), e(128), cu, cu, 2, 8, 8, 4, 1, SCALE, e(128),
+                           torch.empty((0, 2), device="cuda"))
+    dsa.dsa_window_mha_fwd(e(192), e(192), e(128), cu[:1], cu[:1], 0, 0, 0, 4, 1, SCALE, e(128))
+    assert_no_device_error()

@@ -140,3 +140,23 @@ def test_stream_of_another_device_is_refused():
 
     with pytest.raises(ValueError, match="cuda:1"):
         dsa._On(0, Stream())
+
+
+def test_null_addresses_of_empty_tensors():
+    """Nothing to read or write: no address is needed for it."""
+    none = dict(B=0, table=None, lens=None, q=None, out=None, lse=None, m_in=None, m_out=None,
+                mass=None, nt=None, nl=None, idx=None, nm=None)
+    for n in (640, 0):
+        assert decode(**none, max_len=n) == OK
+        assert mass(**none, max_len=n) == OK
+        assert evict(**none, max_len=n) == OK
+    assert mass(max_len=0, m_in=None, m_out=None) == OK
+    # (a sequence without a cache still has an output)
+    assert decode(max_len=0, out=None) == INVALID
+    assert evict(max_len=0, idx=None) == INVALID and evict(max_len=0, nl=None) == INVALID
+    assert mass(**dict(none, B=4)) == INVALID and mass(m_out=None) == INVALID
+    assert window_mha(tq=0, q=None, out=None) == OK
+    assert window_mha(tq=0, tk=0, mlq=0, mlk=0, B=0, q=None, k=None, v=None, out=None) == OK
+    # what is no tensor's address is still looked at
+    assert decode(**none, window=-1) == INVALID and decode(**none, H=8) == UNSUPPORTED
+    assert evict(**none, budget=0) == INVALID and window_mha(tq=0, q=None, H=0) == UNSUPPORTED
