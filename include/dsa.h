@@ -411,7 +411,8 @@ DSA_API size_t dsa_masked_mha_workspace_size(int64_t total_q, int max_len_k);
  *  weight 0 there, so its value must be finite (0 * inf is not 0).
  *  Supported: d_qk = 192, d_v = 128, 1 <= H <= 65535, max_len_k <= 2^24.
  *  A sequence with more queries than keys sets DSA_ERR_BOUNDS and gets no
- *  output.
+ *  output; one with more than max_len_q queries sets it too, and only its
+ *  first max_len_q rows are computed.
  *  Arithmetic: bf16 tensor-core products, fp32 accumulation and softmax (the
  *  weights are rounded to bf16 for the product with the values).
  */

@@ -94,6 +94,7 @@ struct Params {
   const int32_t* cu_k;
   int64_t total_k;
   int B, H;
+  int max_len_q;
   int pairs;                // query-tile pairs per sequence slot
   int window, sinks;        // window 0: no limit
   int items, rounds;        // rounds: items per CTA
@@ -153,7 +154,7 @@ __device__ __forceinline__ Item item_of(const Params& P, int n) {
   const int len_q = __ldg(P.cu_q + x.b + 1) - x.cq;
   x.len_k = __ldg(P.cu_k + x.b + 1) - x.ck;
   x.off = x.len_k - len_q;
-  x.rows = min(2 * kBM, len_q - x.q0);
+  x.rows = min(2 * kBM, min(len_q, P.max_len_q) - x.q0);
   if (none) x.rows = 0;
   x.tiles = x.rows <= 0 || x.off < 0 ? 0 : (x.rows > kBM ? 2 : 1);
   const int p0 = x.off + x.q0, p1 = p0 + x.rows - 1;
@@ -253,8 +254,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
     for (int it = 0; ok && it < P.rounds; ++it) {
       const Item x = item_of(P, it);
-      // (more queries than keys: there is no such sequence)
-      if (x.off < 0 && x.rows > 0 && lane == 0) raise_error(P.err, kErrBounds);
+      // more queries than keys (there is no such sequence), or than the call allows
+      if (lane == 0 && x.rows > 0 &&
+          (x.off < 0 || __ldg(P.cu_q + x.b + 1) - x.cq > P.max_len_q))
+        raise_error(P.err, kErrBounds);
       if (x.tiles == 0) continue;
       auto queries = [&](int t) {
         ok = ok && all_wait(q_empty(t), ((t ? nq1 : nq0) & 1) ^ 1, P.err);
@@ -654,6 +657,7 @@ cudaError_t launch_window_mha(const CUtensorMap& tq, const CUtensorMap& tk, cons
   P.total_k = a.total_k;
   P.B = a.B;
   P.H = a.H;
+  P.max_len_q = a.max_len_q;
   P.pairs = (a.max_len_q + 2 * kBM - 1) / (2 * kBM);
   P.window = a.window;
   P.sinks = a.sinks;

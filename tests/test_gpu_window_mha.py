@@ -205,6 +205,24 @@ def test_more_queries_than_keys_is_reported():
     check(q, k, v, cu_q, cu_k, out, None, 8, 1, seqs=[1])
 
 
+@pytest.mark.parametrize("lens,most", [([250, 100], 200), ([600, 10], 305)])
+def test_more_queries_than_the_bound_is_reported(lens, most):
+    """Rows past max_len_q get no output, and the call says so."""
+    q, k, v, cu_q, cu_k, _ = make(lens, None, 2, seed=89)
+    out = torch.full((sum(lens), 2, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((sum(lens), 2), 7.0, device="cuda")
+    dsa.dsa_window_mha_fwd(q.cuda(), k.cuda(), v.cuda(), cu_q.cuda(), cu_k.cuda(), 2, most,
+                           max(lens), 64, 2, SCALE, out, lse)
+    assert dsa.dsa_get_device_error() == DSA_ERR_BOUNDS
+    assert (out[most:lens[0]] == 7).all() and (lse[most:lens[0]] == 7).all()
+    # the other rows are those of a call that allows the length
+    full, full_lse = call(q, k, v, cu_q, cu_k, lens, lens, 64, 2)
+    assert_no_device_error()
+    out[most:lens[0]], lse[most:lens[0]] = full[most:lens[0]], full_lse[most:lens[0]]
+    for o, l in ((full, full_lse), (out, lse)):
+        check(q, k, v, cu_q, cu_k, o, l, 64, 2)
+
+
 def test_no_queries():
     """Nothing to do, with the null addresses that empty tensors have."""
     cu = torch.zeros(3, dtype=torch.int32, device="cuda")
