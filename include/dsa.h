@@ -442,7 +442,8 @@ DSA_API dsa_status_t dsa_window_mha_fwd(const void* q, const void* k, const void
  *  seq_lens (device) int32 [B]: entries cached per sequence, the newest token's
  *           own among them; 0 is allowed.  Rows of a page behind the length
  *           are never used, whatever they hold.
- *  max_len_k bounds the lengths (at most 2^24).
+ *  max_len_k bounds the lengths (at most 2^24, and B * (max_len_k / 64 + 1)
+ *  below 2^31 - 65536: tiles are counted in 32 bits).
  *  An array without an element (B = 0, or one value per entry and max_len_k = 0)
  *  may be NULL; so may dsa_window_mha_fwd's of total_q = 0.
  *

@@ -752,7 +752,9 @@ dsa_status_t check_cache(const void* kv_cache, int64_t n_pages, int page_size,
   if (page_stride < static_cast<int64_t>(page_size) * 576) return DSA_ERR_INVALID_ARG;
   if (page_stride >= (int64_t(1) << 38)) return DSA_ERR_UNSUPPORTED;
   if (!aligned16(kv_cache) || page_stride % 8 != 0) return DSA_ERR_ALIGNMENT;
-  if (static_cast<int64_t>(B) * (max_len_k / 64 + 1) >= (int64_t(1) << 31))
+  // (the kernels count tiles in 32 bits; the line they stand in is cut into at most
+  // one piece per SM, of up to three tiles more than an equal share)
+  if (static_cast<int64_t>(B) * (max_len_k / 64 + 1) >= (int64_t(1) << 31) - 65536)
     return DSA_ERR_UNSUPPORTED;
   return DSA_OK;
 }

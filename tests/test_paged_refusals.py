@@ -160,3 +160,15 @@ def test_null_addresses_of_empty_tensors():
     # what is no tensor's address is still looked at
     assert decode(**none, window=-1) == INVALID and decode(**none, H=8) == UNSUPPORTED
     assert evict(**none, budget=0) == INVALID and window_mha(tq=0, q=None, H=0) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("B,tiles,status", [(65535, 32768, UNSUPPORTED), (1 << 20, 2048, UNSUPPORTED),
+                                            (65535, 32767, WORKSPACE)])
+def test_more_tiles_than_32_bits_count_are_refused(B, tiles, status):
+    """The tiles of all sequences stand in one line whose positions are 32-bit numbers, those
+    of the last pieces' ends too."""
+    page = 65536
+    big = dict(B=B, max_len=64 * (tiles - 1), page=page, stride=page * 576, pages=40, ld=40, H=16)
+    assert decode(**big, nbytes=16) == status
+    if status == UNSUPPORTED:
+        assert mass(**big, ld_m=64 * tiles) == status
