@@ -260,16 +260,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           P.out[at] = w.k.key(s) ? total + ((sum.x + sum.y) + (sum2.x + sum2.y)) : total;
       }
     }
-    // the entries between the first tokens' tiles and the window's, which no
-    // tile above covers, keep their totals
-    if (P.in != P.out) {
+    // The entries between the first tokens' tiles and the window's, which no
+    // tile above covers, keep their totals (without a window there are none).  The
+    // sequences are spread over the grid's read-out warps, a sequence over several where
+    // these are more.  (With every CTA looking at every sequence 2048 of 100-700 entries, 16
+    // heads, took 921 us with a window of 64 and 378 without, so 110 and 180; 16 of
+    // 4K-128K, 128 heads, window 4096: 37.8, so 24.4.)
+    if (P.in != P.out && P.c.window > 0) {
+      constexpr int kPer = 8;           // loads in flight per lane
+      const int warps = static_cast<int>(gridDim.x) * 4, me = static_cast<int>(blockIdx.x) * 4 + sp;
+      const int split = max(1, warps / P.c.B), step = warps / split;
 #pragma unroll 1
-      for (int b = 0; b < P.c.B; ++b) {
+      for (int b = me < step * split ? me / split : P.c.B; b < P.c.B; b += step) {
         const Seen<kTile> k = seen_of<kTile>(P.c, seq_len(P.c, b));
         const int64_t row = static_cast<int64_t>(b) * P.ld;
+        const int end = k.w0 * kTile;
 #pragma unroll 1
-        for (int s = k.a * kTile + blockIdx.x * 128 + tid; s < k.w0 * kTile; s += gridDim.x * 128)
-          P.out[row + s] = P.in ? P.in[row + s] : 0.f;
+        for (int s = k.a * kTile + me % split * (32 * kPer) + lane; s < end; s += split * (32 * kPer)) {
+          float v[kPer];
+#pragma unroll
+          for (int u = 0; u < kPer; ++u)
+            v[u] = P.in && s + 32 * u < end ? P.in[row + s + 32 * u] : 0.f;
+#pragma unroll
+          for (int u = 0; u < kPer; ++u)
+            if (s + 32 * u < end) P.out[row + s + 32 * u] = v[u];
+        }
       }
     }
   }

@@ -123,3 +123,14 @@ def test_infinite_total_and_nan_entry():
     assert_no_device_error()
     assert torch.isnan(m[0, 50]) and int(torch.isnan(m).sum()) == 1
     assert torch.isinf(m[1, 5]) and int(torch.isinf(m).sum()) == 1
+
+
+@pytest.mark.parametrize("B", [3, 41, 300, 700])
+def test_totals_between_the_first_tokens_and_the_window(B):
+    """Gaps from none to several thousand entries, in more and in fewer sequences than there are
+    warps to copy them."""
+    top = 20000 if B < 10 else 900
+    lens = [(1 + 7919 * i) % top for i in range(B)]
+    lens[-1] = top
+    for window, sinks, no_in in ((60, 1, False), (300, 130, False), (60, 5, True), (0, 0, False)):
+        run(C.Cache(lens, page=16, H=16, seed=47), window, sinks, no_in=no_in)
