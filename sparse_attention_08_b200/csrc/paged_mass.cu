@@ -40,18 +40,19 @@ constexpr int kMaxStages = 12;
 constexpr uint32_t kOffBar = 0;                       // full[12], empty[12], q_full, q_empty, s_full[2], s_empty[2], drain
 constexpr uint32_t kNumBars = 2 * kMaxStages + 7;
 constexpr uint32_t kOffMisc = kNumBars * 8;           // TMEM slot, plan scratch
-constexpr uint32_t kOffLse = (kOffMisc + 96 + 127) / 128 * 128;   // [2][128]: -lse in log2 units
+constexpr uint32_t kOffLse = (kOffMisc + 96 + 127) / 128 * 128;   // [2][128]: -lse
 constexpr uint32_t kOffQ = (kOffLse + 2 * 128 * 4 + 1023) / 1024 * 1024;
 constexpr int kWarps = 8;                             // 2 load, MMA, idle, 4 read-out
 constexpr int kThreads = 32 * kWarps;
 constexpr uint32_t kSmemMax = 232448 - 1024;
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct Params {
   Cache c;
   int H, h0, heads;       // all heads; the launch's first and count
   int n_mma;              // MMA N: heads
   int stages, pieces;
-  float scale_log2;
+  float scale;
   const float* lse;       // [B, H]
   const float* in;        // nullable
   float* out;
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // this segment's -lse, in a buffer that the segment before last used
       float* lse = ml + (seg & 1) * 128;
       if (tid < P.heads)
-        lse[tid] = __ldg(P.lse + static_cast<int64_t>(w.b) * P.H + P.h0 + tid) * -1.4426950408889634f;
+        lse[tid] = -__ldg(P.lse + static_cast<int64_t>(w.b) * P.H + P.h0 + tid);
       // the barrier also takes the four warps out together when a wait gave up
       if (named_bar_or(1, 128, !ok)) {
         ok = false;
@@ -236,7 +237,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         float2 sum = make_float2(0.f, 0.f), sum2 = sum;
-        const float2 sc = make_float2(P.scale_log2, P.scale_log2);
+        // The change to base 2 comes after the difference, so that no error grows with the
+        // scores' size: with scale and lse changed before, at an lse of 290 a weight was off by 8e-6
+        // (all of a head's alike), so by 5e-7.
+        const float2 sc = make_float2(P.scale, P.scale), to2 = make_float2(kLog2e, kLog2e);
 #pragma unroll 1
         for (int h = 0; h < P.n_mma; h += 16) {
           uint32_t v[16];
@@ -245,10 +249,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 16; e += 4) {
             const float4 m = *reinterpret_cast<const float4*>(lse + h + e);
-            const float2 y = __ffma2_rn(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])),
-                                        sc, make_float2(m.x, m.y));
-            const float2 z = __ffma2_rn(make_float2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])),
-                                        sc, make_float2(m.z, m.w));
+            const float2 y = __fmul2_rn(__ffma2_rn(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])),
+                                                   sc, make_float2(m.x, m.y)), to2);
+            const float2 z = __fmul2_rn(__ffma2_rn(make_float2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])),
+                                                   sc, make_float2(m.z, m.w)), to2);
             sum = __fadd2_rn(sum, make_float2(fast_exp2(y.x), fast_exp2(y.y)));
             sum2 = __fadd2_rn(sum2, make_float2(fast_exp2(z.x), fast_exp2(z.y)));
           }
@@ -317,7 +321,7 @@ cudaError_t launch_paged_mass(const CUtensorMap* tq, int launches, const CUtenso
     const int64_t each = (a.max_len_k + kTile - 1) / kTile;
     const int64_t tiles = static_cast<int64_t>(a.cache.B) * (each > 0 ? each : 1);
     P.pieces = static_cast<int>(tiles < a.num_sms ? tiles : a.num_sms);
-    P.scale_log2 = a.sm_scale * 1.4426950408889634f;
+    P.scale = a.sm_scale;
     P.lse = a.lse;
     P.in = i == 0 ? a.in : a.out;
     P.out = a.out;

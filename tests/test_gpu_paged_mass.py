@@ -134,3 +134,28 @@ def test_totals_between_the_first_tokens_and_the_window(B):
     lens[-1] = top
     for window, sinks, no_in in ((60, 1, False), (300, 130, False), (60, 5, True), (0, 0, False)):
         run(C.Cache(lens, page=16, H=16, seed=47), window, sinks, no_in=no_in)
+
+
+def test_weights_of_far_scores_are_as_exact_as_near_ones():
+    """Scores that are exact (whole numbers times 1/16) around a large lse, one head at a time (the
+    others' weights are 0), so that only the exponential rounds: t = score - lse once (2^-24 of
+    t), the change to base 2 by its constant and its product (2^-24 each of t), exp2 by 2^-22
+    of the weight."""
+    n, H, scale = 61, 16, 1.0 / 16
+    c = C.Cache([n], page=16, H=H, seed=48)
+    d = torch.arange(n).float()
+    for s in range(n):
+        c.pool[c.table[0, s // 16].long(), s % 16] = 8.0
+        c.pool[c.table[0, s // 16].long(), s % 16, 0] = 8.0 + d[s]
+    c.q[:] = 1.0
+    pool, table, lens, q = c.to_gpu()
+    at = torch.tensor([288.37, 290.3, 291.77] * 6)[:H]
+    for h in range(H):
+        lse = torch.full((1, H), 1e30)
+        lse[0, h] = at[h]
+        out = torch.zeros((1, n), device="cuda")
+        dsa.dsa_paged_attn_mass(q, pool, table, lens, lse.cuda(), n, scale, out)
+        assert_no_device_error()
+        t = (4608 + d.double()) * scale - lse[0, h].double()
+        off = (out[0].cpu().double() / torch.exp(t) - 1).abs()
+        assert (off <= 3 * 2.0 ** -24 * t.abs() + 2.0 ** -22 + 1e-9).all(), float(off.max())
