@@ -238,8 +238,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         float2 sum = make_float2(0.f, 0.f), sum2 = sum;
         // The change to base 2 comes after the difference, so that no error grows with the
-        // scores' size: with scale and lse changed before, at an lse of 290 a weight was off by 8e-6
-        // (all of a head's alike), so by 5e-7.
+        // scores' size: with scale and lse changed before, a head's
+        // weights at an lse of 290 were all off by 8e-6 alike.
         const float2 sc = make_float2(P.scale, P.scale), to2 = make_float2(kLog2e, kLog2e);
 #pragma unroll 1
         for (int h = 0; h < P.n_mma; h += 16) {

@@ -97,3 +97,20 @@ def check_rows(got, want, tol, what):
     over = ((got - want).abs() - tol)[fin]
     assert over.numel() == 0 or float(over.max()) <= 0, \
         f"{what}: {int((over > 0).sum())} outside, by up to {float(over.max()):.3e}"
+
+
+class SharedPages:
+    """Sequences longer than a pool: block tables that name the pool's pages again and again.
+    row(b): the pool row of each entry of sequence b."""
+
+    def __init__(self, lens, page, n_pages, H, seed):
+        g = torch.Generator().manual_seed(seed)
+        self.lens_list, self.page, self.B, self.H = list(lens), page, len(lens), H
+        self.pool = torch.randn((n_pages, page, D), generator=g).to(torch.bfloat16)
+        cols = -(-max(lens) // page)
+        self.table = torch.randint(0, n_pages, (self.B, cols), generator=g).to(torch.int32)
+        self.q = (torch.randn((self.B, H, D), generator=g) * 2).to(torch.bfloat16)
+
+    def row(self, b):
+        s = torch.arange(self.lens_list[b])
+        return self.table[b].long()[s // self.page] * self.page + s % self.page

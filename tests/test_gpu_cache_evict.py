@@ -204,3 +204,33 @@ def test_cuts_of_cuts_without_a_pause(graph):
     rest = torch.ones(c.n_pages, dtype=torch.bool)
     rest[used] = False
     assert torch.equal(pool[rest.cuda()].view(torch.int16), first[rest.cuda()].view(torch.int16))
+
+
+@pytest.mark.parametrize("lens,budget,kind", [
+    ([262144, 262143, 150000], 8192, "heavy"), ([262144], 262143, "zeros"), ([262144, 262000], 2048, "few"),
+])
+def test_longest_rows(lens, budget, kind):
+    """Rows of the largest size that is allowed, over a pool whose pages they name many times."""
+    page, shared, B = 128, 200, len(lens)
+    per = -(-budget // page)
+    c = C.SharedPages(lens, page, shared + B * per, 16, seed=74)
+    c.table %= shared
+    new_table = shared + torch.randperm(B * per, generator=torch.Generator().manual_seed(75)).reshape(B, per).to(torch.int32)
+    c.max_len = 262144
+    m = totals(c, 76, kind)
+    pool = c.pool.cuda()
+    idx = torch.empty((B, budget), dtype=torch.int32, device="cuda")
+    new_n = torch.empty(B, dtype=torch.int32, device="cuda")
+    new_m = torch.empty((B, budget), device="cuda")
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    dsa.dsa_cache_evict(pool, c.table.cuda(), n, m.cuda(), 262144, budget, 4, 1000, new_table.cuda(), new_n, idx, new_m)
+    assert_no_device_error()
+    assert new_n.tolist() == [min(k, budget) for k in lens]
+    want = c.pool.reshape(-1, 576).clone()
+    for b, k in enumerate(lens):
+        keep = torch.tensor(keep_of(m[b], k, budget, 4, 1000))
+        assert torch.equal(idx[b].cpu().long(), keep)
+        assert torch.equal(new_m[b].cpu().view(torch.int32), m[b, keep].view(torch.int32))
+        j = torch.arange(keep.numel())
+        want[new_table[b].long()[j // page] * page + j % page] = c.pool.reshape(-1, 576)[c.row(b)[keep]]
+    assert torch.equal(pool.cpu().view(torch.int16), want.reshape(pool.shape).view(torch.int16))

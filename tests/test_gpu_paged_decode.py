@@ -201,3 +201,40 @@ def test_out_of_range_lengths_and_pages_are_reported():
     want, _, tol, _ = C.attention64(c.q[1], c.rows(1), C.seen(60, 0, 0))
     C.check_rows(out[1], want, tol, "the sequence beside it")
     assert dsa.dsa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("lens,H,window,sinks", [
+    ([131072], 128, 0, 0),                          # one full context
+    ([1 << 24, (1 << 24) - 37], 16, 0, 0),          # the longest that are allowed
+    ([(1 << 24) - 1], 64, (1 << 23) + 5, 1000),
+])
+def test_longest_sequences(lens, H, window, sinks):
+    """Against 64 bits with each pool row weighted by how often it is seen.  Beside the
+    tolerances of the short cases: O adds up 4 products of 16 keys for each of a CTA's tiles, each off
+    by at most 2^-22 of the sum of magnitudes; a thread adds its weights of every other tile
+    (2^-24 each), and the parts (at most 148) are added up once more.  Head 0 has no query: its
+    weights are all 1, so that its lse counts the entries (to 4 units in its last place)."""
+    c = C.SharedPages(lens, 64, 400, H, seed=35)
+    c.q[:, 0] = 0
+    out = torch.empty((c.B, H, 512), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((c.B, H), device="cuda")
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    dsa.dsa_paged_mla_decode(c.q.cuda(), c.pool.cuda(), c.table.cuda(), n, max(lens), C.SCALE, out, lse,
+                             window=window, sinks=sinks)
+    assert_no_device_error()
+    tiles = sum(lens) // 64 // (148 // -(-H // 64)) + 8
+    for b in range(c.B):
+        row = c.row(b)[torch.from_numpy(C.seen(lens[b], window, sinks))]
+        often = torch.bincount(row, minlength=400 * 64).double()
+        q, x = c.q[b].double(), c.pool.reshape(-1, 576).double()
+        s = C.SCALE * (q @ x.T)
+        want_l = torch.logsumexp(s + often.log(), 1)
+        p = torch.exp(s - want_l[:, None]) * often
+        o, spread = p @ x[:, :512], p @ x[:, :512].abs()
+        d = (576 * 2.0 ** -23 * C.SCALE * (q.abs() @ x.abs().T)).amax(1) + 2.0 ** -21 * s.abs().amax(1)
+        sums = (tiles / 2 + 200) * 2.0 ** -24
+        tol = 2.0 ** -8 * o.abs() + (2.0 ** -7 * 1.02 + 2.1 * d[:, None] + 4 * tiles * 2.0 ** -22 + sums) * spread
+        C.check_rows(out[b], o, tol, f"out of sequence {b}")
+        C.check_rows(lse[b], want_l, d + sums + 2.0 ** -21 + 2.0 ** -21 * want_l.abs(), f"lse of sequence {b}")
+        count = float(torch.tensor(float(row.numel())).double().log())
+        assert abs(float(lse[b, 0]) - count) <= 4 * 2.0 ** -19, "entries seen"

@@ -159,3 +159,24 @@ def test_weights_of_far_scores_are_as_exact_as_near_ones():
         t = (4608 + d.double()) * scale - lse[0, h].double()
         off = (out[0].cpu().double() / torch.exp(t) - 1).abs()
         assert (off <= 3 * 2.0 ** -24 * t.abs() + 2.0 ** -22 + 1e-9).all(), float(off.max())
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), ((1 << 23) + 5, 1000)])
+def test_longest_sequences_entry_by_entry(window, sinks):
+    """One head without a query and with lse = 0 (the others' weights are 0): every entry that is
+    seen gets exactly 1."""
+    lens = [1 << 24, (1 << 24) - 37]
+    c = C.SharedPages(lens, 64, 400, 16, seed=49)
+    c.q[:, 5] = 0
+    lse = torch.full((2, 16), 1e30)
+    lse[:, 5] = 0
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    m = torch.full((2, 1 << 24), 2.0, device="cuda")
+    out = torch.full((2, 1 << 24), -7.0, device="cuda")
+    dsa.dsa_paged_attn_mass(c.q.cuda(), c.pool.cuda(), c.table.cuda(), n, lse.cuda(), 1 << 24, C.SCALE, out,
+                            mass_in=m, window=window, sinks=sinks)
+    assert_no_device_error()
+    for b, k in enumerate(lens):
+        want = torch.full((1 << 24,), -7.0)
+        want[:k] = 2.0 + torch.from_numpy(C.seen(k, window, sinks)).float()
+        assert torch.equal(out[b].cpu(), want)

@@ -179,3 +179,30 @@ def test_empty_batches():
         assert (out == 0).all() and torch.isneginf(lse).all()
         assert (new_n == 0).all() and (idx == -1).all() and (new_mass == 0).all()
     assert torch.isnan(pool.float()).all()
+
+
+def test_pages_far_apart():
+    """Offsets that pass 32 bits: pages 2^27 elements apart (a page of many layers), the last ones
+    5 GB behind the first."""
+    budget, window, sinks = 64, 100, 3
+    c = C.Cache([300, 170], page=16, H=H, seed=92, extra_pages=8)
+    far = torch.empty((c.n_pages, 1 << 27), dtype=torch.bfloat16, device="cuda")
+    pool = far[:, :16 * 576].view(c.n_pages, 16, 576)
+    pool.copy_(c.pool)
+    table, n, q = c.table.cuda(), c.lens.cuda(), c.q.cuda()
+    o, ls = torch.empty((2, H, 512), dtype=torch.bfloat16, device="cuda"), torch.empty((2, H), device="cuda")
+    mass = torch.zeros((2, 300), device="cuda")
+    dsa.dsa_paged_mla_decode(q, pool, table, n, 300, C.SCALE, o, ls, window=window, sinks=sinks)
+    dsa.dsa_paged_attn_mass(q, pool, table, n, ls, 300, C.SCALE, mass, mass_in=mass, window=window, sinks=sinks)
+    free = c.free_pages[:8].reshape(2, 4)
+    idx, new_n = torch.empty((2, budget), dtype=torch.int32, device="cuda"), torch.empty_like(n)
+    dsa.dsa_cache_evict(pool, table, n, mass, 300, budget, 4, 16, free.cuda(), new_n, idx)
+    assert_no_device_error()
+    for b, k in enumerate(c.lens_list):
+        want, wl, tol, tol_l = C.attention64(c.q[b], c.rows(b), C.seen(k, window, sinks))
+        C.check_rows(o[b], want, tol, f"out of sequence {b}")
+        C.check_rows(ls[b], wl, tol_l, f"lse of sequence {b}")
+        got = pool[free[b].long().cuda()].reshape(-1, 576)[:budget].cpu()
+        kept = idx[b].cpu().long()
+        assert kept.tolist()[:4] == [0, 1, 2, 3] and kept.tolist()[-16:] == list(range(k - 16, k))
+        assert torch.equal(got.view(torch.int16), c.rows(b)[kept].view(torch.int16))

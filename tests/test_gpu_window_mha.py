@@ -231,3 +231,24 @@ def test_no_queries():
                            torch.empty((0, 2), device="cuda"))
     dsa.dsa_window_mha_fwd(e(192), e(192), e(128), cu[:1], cu[:1], 0, 0, 0, 4, 1, SCALE, e(128))
     assert_no_device_error()
+
+
+def test_rows_behind_two_billion_elements():
+    """A short sequence behind a long one: its rows' offsets pass 32 bits."""
+    lens, H = [88000, 300], 128
+    T = sum(lens)
+    t = [torch.zeros((T, H, d), dtype=torch.bfloat16, device="cuda") for d in (192, 192, 128)]
+    q, k, v, _, _, _ = make([300], None, H, seed=90)
+    for a, b in zip(t, (q, k, v)):
+        a[88000:] = b.cuda()
+    cu = torch.tensor([0, 88000, T], dtype=torch.int32, device="cuda")
+    out = torch.full((T, H, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, H), 7.0, device="cuda")
+    dsa.dsa_window_mha_fwd(*t, cu, cu, 2, 88000, 88000, 40, 2, SCALE, out, lse)
+    assert_no_device_error()
+    one = torch.tensor([0, 300], dtype=torch.int32)
+    check(q, k, v, one, one, out[88000:], lse[88000:], 40, 2)
+    # zeros before it: the values' zeros, and the log of how many keys a row sees
+    assert (out[:88000] == 0).all()
+    seen = torch.arange(1, 88001, device="cuda").clamp_max(42).double().log()
+    assert float((lse[:88000].double() - seen[:, None]).abs().max()) <= 2.0 ** -20 * 4
