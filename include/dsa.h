@@ -407,14 +407,19 @@ DSA_API size_t dsa_masked_mha_workspace_size(int64_t total_q, int max_len_k);
  *  v        (device) bf16 [total_k, H, 128]
  *  out      (device) bf16 [total_q, H, 128]
  *  lse      (device, nullable) f32 [total_q, H] (natural log)
- *  A key outside a row's window that shares a 128-key tile with one inside has
- *  weight 0 there, so its value must be finite (0 * inf is not 0).
+ *  A key that a row does not see (outside its window or behind its position)
+ *  may share a 128-key tile with one that it sees, and has weight 0 there: its
+ *  value must be finite (0 * inf is not 0).
  *  Supported: d_qk = 192, d_v = 128, 1 <= H <= 65535, max_len_k <= 2^24.
  *  A sequence with more queries than keys sets DSA_ERR_BOUNDS and gets no
  *  output; one with more than max_len_q queries sets it too, and only its
  *  first max_len_q rows are computed.
  *  Arithmetic: bf16 tensor-core products, fp32 accumulation and softmax (the
- *  weights are rounded to bf16 for the product with the values).
+ *  weights are rounded to bf16 for the product with the values).  A row's weights
+ *  are taken over a reference that moves only when they add up to more than 2^32 in
+ *  a tile (or its first to less than 2^-32), so values other than 0 should lie
+ *  between 2^-90 and 2^70 in size: beyond, the fp32 sums of weighted values
+ *  can overflow, or lose small ones, where the definition does not.
  */
 DSA_API dsa_status_t dsa_window_mha_fwd(const void* q, const void* k, const void* v,
                                         const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
@@ -444,6 +449,8 @@ DSA_API dsa_status_t dsa_window_mha_fwd(const void* q, const void* k, const void
  *           are never used, whatever they hold.
  *  max_len_k bounds the lengths (at most 2^24, and B * (max_len_k / 64 + 1)
  *  below 2^31 - 65536: tiles are counted in 32 bits).
+ *  kv_cache, q, out and the workspace are 16-byte aligned; block tables (which
+ *  may be slices), lengths, lse, totals and positions need 4 bytes.
  *  An array without an element (B = 0, or one value per entry and max_len_k = 0)
  *  may be NULL; so may dsa_window_mha_fwd's of total_q = 0.
  *
@@ -473,9 +480,11 @@ DSA_API dsa_status_t dsa_window_mha_fwd(const void* q, const void* k, const void
  *  Supported: d_qk = 576, d_v = 512, H in {16, 32} or a multiple of 64 up to
  *  256.
  *  Arithmetic: bf16 tensor-core products, fp32 accumulation and softmax (the
- *  weights are rounded to bf16 for the product with the values).  The result
- *  does not depend on timing: a sequence split over the GPU is joined in a
- *  fixed order.
+ *  weights are rounded to bf16 for the product with the values).  A head's weights
+ *  are taken over a reference that moves only when they exceed 2^32, so values
+ *  should stay below 2^70 in size: beyond, the fp32 sums of weighted values can
+ *  overflow where the definition does not.  The result does not depend on timing: a
+ *  sequence split over the GPU is joined in a fixed order.
  */
 DSA_API dsa_status_t dsa_paged_mla_decode(const void* q, const void* kv_cache, int64_t n_pages,
                                           int page_size, int64_t page_stride,
@@ -534,7 +543,12 @@ DSA_API dsa_status_t dsa_paged_attn_mass(const void* q, const void* kv_cache, in
  *           new_block_table + b * new_block_table_ld; covers
  *           min(budget, max_len_k) entries.  Its pages must be different from
  *           one another and from every page that a sequence of the call
- *           still reads (the copies run in no order).
+ *           still reads: the copies run in no order, all at once, so a latent
+ *           could be overwritten before it has been read.  For the same reason the
+ *           sequences that keep everything are copied too: the new table alone
+ *           describes the cut cache, and all the old pages are free after it.
+ *           (A caller without room for them cuts only the sequences that are
+ *           over the budget, or a few at a time.)
  *  new_lens (device) int32 [B]: min(n, budget); not seq_lens itself
  *  idx_out  (device) int32 [B, budget]: the kept entries' old positions,
  *           ascending, padded with -1 (to cut other per-entry data alike)

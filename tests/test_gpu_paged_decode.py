@@ -238,3 +238,17 @@ def test_longest_sequences(lens, H, window, sinks):
         C.check_rows(lse[b], want_l, d + sums + 2.0 ** -21 + 2.0 ** -21 * want_l.abs(), f"lse of sequence {b}")
         count = float(torch.tensor(float(row.numel())).double().log())
         assert abs(float(lse[b, 0]) - count) <= 4 * 2.0 ** -19, "entries seen"
+
+
+def test_large_values_under_a_reference_left_behind():
+    """The stated range: values up to 2^70, with weights that grow to 2^31 over a sequence's first."""
+    c = C.Cache([1500], page=16, H=16, seed=36)
+    c.q[..., :512] = 0
+    c.q[..., 512:] = c.q[:, :1, 512:]
+    rope = c.q[0, 0, 512:].float()
+    up = torch.linspace(0, 31 * 0.6931, 1500)[:, None] * rope / (C.SCALE * float(rope @ rope))
+    for s in range(1500):
+        c.pool[c.table[0, s // 16].long(), s % 16, :512] *= 2.0 ** 68
+        c.pool[c.table[0, s // 16].long(), s % 16, 512:] = up[s].to(torch.bfloat16)
+    assert float(c.rows(0)[:, :512].abs().max()) <= 2.0 ** 70 + 2.0 ** 69
+    check(c, *run(c))

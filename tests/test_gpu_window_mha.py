@@ -252,3 +252,19 @@ def test_rows_behind_two_billion_elements():
     assert (out[:88000] == 0).all()
     seen = torch.arange(1, 88001, device="cuda").clamp_max(42).double().log()
     assert float((lse[:88000].double() - seen[:, None]).abs().max()) <= 2.0 ** -20 * 4
+
+
+@pytest.mark.parametrize("v_mul,ramp", [(2.0 ** 68, (0.0, 31.0)), (2.0 ** -90, (-31.0, -28.0))])
+def test_large_and_small_values_under_a_reference_left_behind(v_mul, ramp):
+    """The stated range: values from 2^-90 to 2^70, with a row's weights from 2^-31 to 2^31."""
+    q, k, v, cu_q, cu_k, lens_q = make([500], None, 2, seed=91)
+    q[:] = q[:1]
+    up = torch.linspace(*ramp, 500)[:, None] * 0.6931
+    for h in range(2):
+        x = q[0, h].float()
+        k[:, h] = (up * x / (SCALE * float(x @ x))).to(torch.bfloat16)
+    v *= v_mul
+    for window, sinks in ((0, 0), (200, 4)):
+        out, lse = call(q, k, v, cu_q, cu_k, lens_q, [500], window, sinks)
+        assert_no_device_error()
+        check(q, k, v, cu_q, cu_k, out, lse, window, sinks)
