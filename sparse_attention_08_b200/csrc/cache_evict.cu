@@ -343,7 +343,7 @@ cudaError_t launch_select(const Params& P, size_t smem, cudaStream_t s) {
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  // (its start under the end of the kernel before: two calls in a row 16.4 -> 15.1 us
+  // (its start under the end of the kernel before: two calls in a row 16.4 -> 14.5 us
   // for one row of 131072; the attention kernels gain nothing by it, and the decode
   // lost 4 % where two CTAs read the same keys)
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;

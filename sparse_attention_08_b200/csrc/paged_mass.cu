@@ -20,7 +20,7 @@
 // tile overlap the products of the next.  One read of the cache (1152 bytes an
 // entry) bounds it: the 36 MMAs of a tile take 2300 cycles at N = 128, its bytes
 // about 6300 of an SM's share of the memory.  16 sequences of 4K-128K (1.18 GB), 128
-// heads: 202-222 us, 5.3-5.8 TB/s.
+// heads: 198-222 us, 5.3-6.0 TB/s.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
