@@ -45,8 +45,9 @@
  *  every wait; a wait that runs out sets a device error word and that launch
  *  returns early.  An input error found on the device (DSA_ERR_BOUNDS) is
  *  reported in the same word and ends nothing.  Neither touches other launches,
- *  replays of captured ones among them.  dsa_get_device_error() reads and
- *  clears the word.
+ *  replays of captured ones among them; only a captured launch that has itself
+ *  timed out gives up early again until the word is cleared.
+ *  dsa_get_device_error() reads and clears the word.
  */
 #ifndef DSA_H_
 #define DSA_H_
